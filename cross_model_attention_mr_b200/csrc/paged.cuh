@@ -1,0 +1,43 @@
+// Device side of the paged cache: page lookup and the row a position lives in.
+#pragma once
+
+#include "paged.h"
+
+namespace mr {
+
+__device__ __forceinline__ uint32_t fast_div(uint32_t n, const FastDiv& f) {
+  return (__umulhi(n, f.mul) + n) >> f.shift;
+}
+
+// Detail codes recorded beside MR_ERR_DEVICE_CHECK.
+constexpr uint32_t kBadPage = 0xD01;      // page number outside the pool
+constexpr uint32_t kTableShort = 0xD02;   // kv_len beyond the table
+constexpr uint32_t kBadPair = 0xD03;      // page pair outside the pool, or in conflict with another
+
+// Pool row of (sequence s, kv head g, row j < capacity), or -1 for a page outside the pool.  Rows are
+// numbered over the whole pool (the host keeps that below 2^31); row r starts at r * d elements.
+__device__ __forceinline__ int pool_row(const PagedKv& kv, int s, int g, int j) {
+  const int pi = (int)fast_div((uint32_t)j, kv.by_rows);
+  const int page = __ldg(kv.table + (int64_t)s * kv.pages_per_seq + pi);
+  if ((uint32_t)page >= (uint32_t)kv.n_pages) return -1;
+  return (page * kv.H_kv + g) * kv.page_rows + (j - pi * kv.page_rows);
+}
+
+// Sequence of packed row t: the s with cu[s] <= t < cu[s + 1], or n_seq when t is behind the last one.
+// Whole warp; cu ascends.  One round of 32 probes narrows the range 32-fold (a probe that finds
+// cu[i + 1] <= t leaves every sequence up to i behind).
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int n_seq, int t, int lane) {
+  int lo = 0, hi = n_seq;  // the answer lies in [lo, hi]
+  while (hi > lo) {
+    const int step = (hi - lo + 31) / 32;
+    const int i = lo + (lane + 1) * step - 1;
+    const bool behind = i < hi && __ldg(cu + i + 1) <= t;
+    const int c = __popc(__ballot_sync(0xffffffffu, behind));
+    const int nlo = lo + c * step;
+    hi = min(hi, nlo + step - 1);
+    lo = min(nlo, hi);
+  }
+  return lo;
+}
+
+}  // namespace mr

@@ -18,7 +18,13 @@ enum KernelId {
   kKWaitProbe = 10,
   kKPrep = 11,
   kKGatherProbe = 12,
-  kNumKernelIds = 13
+  kKRope = 13,
+  kKAppend = 14,
+  kKDecode = 15,
+  kKAttn = 16,
+  kKAttnTc = 17,
+  kKPagesCopy = 18,
+  kNumKernelIds = 19
 };
 
 // Called immediately before and after each kernel launch on `st`.

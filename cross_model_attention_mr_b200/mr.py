@@ -8,6 +8,7 @@ there is no fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -45,6 +46,24 @@ class BSR(ctypes.Structure):
                 ("tile_scale", _c_p), ("renormalised", _c_i32)]
 
 
+class Rows(ctypes.Structure):
+    _fields_ = [("ptr", _c_p), ("head_stride", _c_i64), ("row_stride", _c_i64)]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", _c_p), ("v", _c_p), ("dt", ctypes.c_int), ("H_kv", _c_i32), ("page_rows", _c_i32),
+                ("d", _c_i32), ("n_pages", _c_i64)]
+
+
+class KvSeqs(ctypes.Structure):
+    _fields_ = [("table", _c_p), ("kv_len", _c_p), ("pages_per_seq", _c_i32), ("n_seq", _c_i32)]
+
+
+class RopeTable(ctypes.Structure):
+    _fields_ = [("d", _c_i32), ("rot_dim", _c_i32), ("interleaved", _c_i32), ("mscale", _c_f32),
+                ("turn", ctypes.c_uint64 * 128)]
+
+
 EXPORTS = {
     "mr_version": ([], ctypes.c_int),
     "mr_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -79,6 +98,29 @@ EXPORTS = {
     "mr_bm_release": ([_c_p, _c_i64], ctypes.c_int),
     "mr_bm_evicted": ([_c_p, ctypes.POINTER(_c_i64), ctypes.c_int], ctypes.c_int),
     "mr_bm_stats": ([_c_p, ctypes.POINTER(_c_i64)], ctypes.c_int),
+    "mr_rope_init": ([ctypes.POINTER(RopeTable), ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_double, ctypes.c_int,
+                      ctypes.c_double, ctypes.c_int, ctypes.c_double, ctypes.c_double, ctypes.c_double, _c_p],
+                     ctypes.c_int),
+    "mr_rope_apply": ([ctypes.POINTER(RopeTable), ctypes.POINTER(Rows), ctypes.POINTER(Rows), ctypes.c_int,
+                       ctypes.c_int, ctypes.c_int, _c_p, ctypes.c_int, _c_p], ctypes.c_int),
+    "mr_paged_workspace_bytes": ([ctypes.POINTER(KvCache), ctypes.c_int, ctypes.c_int], _c_sz),
+    "mr_kv_append": ([ctypes.POINTER(KvCache), ctypes.POINTER(KvSeqs), ctypes.POINTER(RopeTable), ctypes.POINTER(Rows),
+                      ctypes.POINTER(Rows), ctypes.c_int, ctypes.POINTER(Rows), ctypes.POINTER(Rows), _c_p, ctypes.c_int,
+                      _c_p, _c_sz, _c_p], ctypes.c_int),
+    "mr_pages_copy_workspace_bytes": ([], _c_sz),
+    "mr_pages_copy": ([ctypes.POINTER(_c_p), ctypes.c_int, _c_i64, _c_i64, _c_p, ctypes.c_int, _c_p, _c_sz, _c_p],
+                      ctypes.c_int),
+    "mr_pp_create": ([ctypes.c_int, ctypes.c_int], _c_p),
+    "mr_pp_destroy": ([_c_p], None),
+    "mr_pp_open": ([_c_p], _c_i64),
+    "mr_pp_fork": ([_c_p, _c_i64, ctypes.c_int], _c_i64),
+    "mr_pp_extend": ([_c_p, _c_i64, ctypes.c_int, _c_p], ctypes.c_int),
+    "mr_pp_truncate": ([_c_p, _c_i64, ctypes.c_int], ctypes.c_int),
+    "mr_pp_slide": ([_c_p, _c_i64, ctypes.c_int, ctypes.c_int], ctypes.c_int),
+    "mr_pp_close": ([_c_p, _c_i64], ctypes.c_int),
+    "mr_pp_compact": ([_c_p, _c_p, ctypes.c_int], ctypes.c_int),
+    "mr_pp_table": ([_c_p, _c_i64, _c_p, ctypes.c_int, ctypes.POINTER(ctypes.c_int)], ctypes.c_int),
+    "mr_pp_stats": ([_c_p, ctypes.POINTER(_c_i64)], ctypes.c_int),
     "mr_gather_probe": ([ctypes.POINTER(BSR), ctypes.c_int, ctypes.c_int, _c_p, _c_sz, _c_p], ctypes.c_int),
     "mr_debug_set": ([ctypes.c_uint64, ctypes.c_int], ctypes.c_int),
     "mr_profile_enable": ([ctypes.c_int], ctypes.c_int),
@@ -556,3 +598,260 @@ class BlockManager:
         v = (_c_i64 * 5)()
         check(LIB.mr_bm_stats(self.h, v), "mr_bm_stats")
         return dict(zip(("entries", "bytes", "lookups", "hits", "hit_blocks"), [int(x) for x in v]))
+
+
+# ------------------------------------------------------------------------------------------------
+# The receiver's paged key-value cache (MapFlow section 6): rotary positions, appending rows,
+# attention of new rows over the cache, copying pages, and the host-side page pool.
+# These calls run on the device of their tensors, whichever device is current.
+# ------------------------------------------------------------------------------------------------
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def _on_device_of(t: torch.Tensor):
+    """Context that makes the device of `t` current (the library launches on the current device)."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    return _NO_SWITCH if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _rows(t: torch.Tensor, like: torch.Tensor, what: str) -> Rows:
+    """mr_rows of a [heads][rows][d] tensor with any strides over heads and rows."""
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{what} must be [heads][rows][d] with adjacent elements in a row")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{what} must have dtype {like.dtype}")
+    if t.device != like.device:
+        raise ValueError(f"{what} must be on {like.device}")
+    return Rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _ints(t: torch.Tensor, like: torch.Tensor, what: str, dim: int = 1) -> int:
+    """Address of a contiguous int32 tensor on the device of `like`."""
+    if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of {dim} dimension(s)")
+    if t.device != like.device:
+        raise ValueError(f"{what} must be on {like.device}")
+    return t.data_ptr()
+
+
+class Rope:
+    """Rotary positions of the first `rot_dim` of d elements (mr_rope_init).  ``scaling`` is "none",
+    "linear", "base" or "ramp" with ``factor`` (and ``orig_len``, ``beta_slow``, ``beta_fast`` for the
+    ramp); ``inv_freq`` gives the angles per position directly.  Host data only: keep and reuse it."""
+
+    SCALING = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
+
+    def __init__(self, d: int, rot_dim: Optional[int] = None, base: float = 10000.0, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0, orig_len: int = 0, beta_slow: float = 1.0,
+                 beta_fast: float = 32.0, mscale: float = 1.0, inv_freq=None):
+        self.d, self.rot_dim = int(d), int(d if rot_dim is None else rot_dim)
+        if scaling not in self.SCALING:
+            raise ValueError(f"scaling must be one of {sorted(self.SCALING)}")
+        freq = None
+        if inv_freq is not None:
+            freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+            if freq.shape != (self.rot_dim // 2,):
+                raise ValueError("inv_freq must hold rot_dim / 2 angles")
+        self.c = RopeTable()
+        check(LIB.mr_rope_init(ctypes.byref(self.c), self.d, self.rot_dim, int(interleaved), float(base),
+                               self.SCALING[scaling], float(factor), int(orig_len), float(beta_slow), float(beta_fast),
+                               float(mscale), freq.ctypes.data if freq is not None else None), "mr_rope_init")
+
+
+def rope(r: Rope, X: torch.Tensor, pos: torch.Tensor, out: Optional[torch.Tensor] = None, adjoint: bool = False,
+         stream=None) -> torch.Tensor:
+    """mr_rope_apply: X [H][rows][d] (any strides over heads and rows) rotated by each row's position
+    (int32, device).  ``out=X`` rotates in place; ``adjoint=True`` gives the gradient with respect to X
+    for a gradient with respect to the result."""
+    with _on_device_of(X):
+        dt = _dt(X)
+        x = _rows(X, X, "X")
+        H, n, d = X.shape
+        if d != r.d:
+            raise ValueError(f"rows of {d} elements, rotation for {r.d}")
+        if pos.shape[0] != n:
+            raise ValueError("pos must give one position per row")
+        if out is None:
+            out = torch.empty((H, n, d), dtype=X.dtype, device=X.device)
+        elif out.shape != X.shape:
+            raise ValueError("out must have the shape of X")
+        check(LIB.mr_rope_apply(ctypes.byref(r.c), ctypes.byref(x), ctypes.byref(_rows(out, X, "out")), dt, H, n,
+                                _ints(pos, X, "pos"), 1 if adjoint else 0, _stream(stream)), "mr_rope_apply")
+    return out
+
+
+class KVCache:
+    """A pool of pages: k and v, each [n_pages][H_kv][page_rows][d] (bf16 or fp32, contiguous, CUDA)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        _need_cuda(k, v)
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must both be [n_pages][H_kv][page_rows][d], of one dtype, on one device")
+        self.k, self.v = k, v
+        self.n_pages, self.H_kv, self.page_rows, self.d = k.shape
+        self.c = KvCache(k.data_ptr(), v.data_ptr(), _dt(k), self.H_kv, self.page_rows, self.d, self.n_pages)
+
+    @classmethod
+    def empty(cls, n_pages: int, H_kv: int, page_rows: int, d: int, dtype=torch.bfloat16, device="cuda") -> "KVCache":
+        """A new cache whose pages hold nothing yet."""
+        shape = (n_pages, H_kv, page_rows, d)
+        return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device))
+
+
+def _seqs(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor) -> KvSeqs:
+    n = kv_len.shape[0]
+    t, l = _ints(table, cache.k, "table", 2), _ints(kv_len, cache.k, "kv_len")
+    if table.shape[0] != n:
+        raise ValueError("table must have one row per sequence")
+    return KvSeqs(t, l, table.shape[1], n)
+
+
+def paged_workspace_bytes(cache: KVCache, H_q: int, n_seq: int) -> int:
+    return int(LIB.mr_paged_workspace_bytes(ctypes.byref(cache.c), int(H_q), int(n_seq)))
+
+
+def kv_append(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
+              cu_q: Optional[torch.Tensor] = None, rope: Optional[Rope] = None, Q: Optional[torch.Tensor] = None,
+              q_out: Optional[torch.Tensor] = None, ws: Optional[Workspace] = None,
+              stream=None) -> Optional[torch.Tensor]:
+    """mr_kv_append: store the new rows K, V [H_kv][total_q][d] (K rotated) in the pages that table
+    [n_seq][pages_per_seq] names, ending at kv_len [n_seq], and return Q [H_q][total_q][d] rotated (None
+    without Q; ``q_out=Q`` rotates in place).  ``cu_q`` [n_seq + 1]: rows of each sequence (None: one each)."""
+    with _on_device_of(cache.k):
+        k, v = _rows(K, cache.k, "K"), _rows(V, cache.k, "V")
+        total = K.shape[1]
+        if K.shape != V.shape or K.shape[0] != cache.H_kv or K.shape[2] != cache.d:
+            raise ValueError("K and V must be [H_kv][total_q][d] of the cache")
+        q = qo = None
+        H_q = 0
+        if Q is not None:
+            H_q = Q.shape[0]
+            if Q.shape[1:] != K.shape[1:]:
+                raise ValueError("Q must be [H_q][total_q][d]")
+            if q_out is None:
+                q_out = torch.empty((H_q, total, cache.d), dtype=Q.dtype, device=Q.device)
+            elif q_out.shape != Q.shape:
+                raise ValueError("q_out must have the shape of Q")
+            q, qo = ctypes.byref(_rows(Q, cache.k, "Q")), ctypes.byref(_rows(q_out, cache.k, "q_out"))
+        elif q_out is not None:
+            raise ValueError("q_out without Q")
+        seqs = _seqs(cache, table, kv_len)
+        if cu_q is not None and cu_q.shape[0] != seqs.n_seq + 1:
+            raise ValueError("cu_q must have n_seq + 1 entries")
+        if ws is None:
+            ws = Workspace(paged_workspace_bytes(cache, cache.H_kv, seqs.n_seq), cache.k.device)
+        check(LIB.mr_kv_append(ctypes.byref(cache.c), ctypes.byref(seqs), ctypes.byref(rope.c) if rope else None, q, qo,
+                               H_q, ctypes.byref(k), ctypes.byref(v),
+                               _ints(cu_q, cache.k, "cu_q") if cu_q is not None else None, total, ws.ptr, ws.nbytes,
+                               _stream(stream)), "mr_kv_append")
+    return q_out
+
+
+def pages_copy_workspace_bytes() -> int:
+    return int(LIB.mr_pages_copy_workspace_bytes())
+
+
+def pages_copy(pools, pairs: torch.Tensor, ws: Optional[Workspace] = None, stream=None) -> None:
+    """mr_pages_copy: page pairs[t][1] <- page pairs[t][0] (int32, device) in every pool (tensors
+    [n_pages][...], e.g. the k and v of every layer's cache)."""
+    first = pools[0]
+    with _on_device_of(first):
+        page_bytes = first.stride(0) * first.element_size()
+        for t in pools:
+            _need_cuda(t)
+            if t.shape[0] != first.shape[0] or t.device != first.device or t.stride(0) * t.element_size() != page_bytes:
+                raise ValueError("pools must have the same pages on the same device")
+        p = _ints(pairs, first, "pairs", 2)
+        if pairs.shape[1] != 2:
+            raise ValueError("pairs must be [n][2]")
+        if ws is None:
+            ws = Workspace(pages_copy_workspace_bytes(), first.device)
+        ptrs = (_c_p * len(pools))(*[t.data_ptr() for t in pools])
+        check(LIB.mr_pages_copy(ptrs, len(pools), page_bytes, first.shape[0], p, pairs.shape[0], ws.ptr, ws.nbytes,
+                                _stream(stream)), "mr_pages_copy")
+
+
+class PagePool:
+    """mr_pp_*: which pages of a pool each sequence holds (host only), with shared pages after a fork.
+
+    ``extend`` and ``compact`` return (source, destination) pairs; copy them with ``pages_copy`` before the
+    pages are used again."""
+
+    def __init__(self, n_pages: int, page_rows: int):
+        self.h = LIB.mr_pp_create(int(n_pages), int(page_rows))
+        if not self.h:
+            raise MRError(MR_ERR_INVALID_ARG, "mr_pp_create")
+        self.n_pages, self.page_rows = int(n_pages), int(page_rows)
+
+    def __del__(self):
+        if getattr(self, "h", None) and LIB is not None:  # LIB is gone while the interpreter ends
+            LIB.mr_pp_destroy(self.h)
+        self.h = None
+
+    @staticmethod
+    def _count(n, where: str) -> int:
+        if n < 0:
+            raise MRError(-int(n), where)
+        return int(n)
+
+    def open(self) -> int:
+        return self._count(LIB.mr_pp_open(self.h), "mr_pp_open")
+
+    def fork(self, seq: int, rows: int) -> int:
+        """New sequence that shares the first `rows` rows of `seq`."""
+        return self._count(LIB.mr_pp_fork(self.h, int(seq), int(rows)), "mr_pp_fork")
+
+    def extend(self, seq: int, rows: int) -> list:
+        """Room for `rows` more rows; the list holds one pair when a shared page has to be copied first."""
+        pair = (_c_i32 * 2)()
+        n = self._count(LIB.mr_pp_extend(self.h, int(seq), int(rows), pair), "mr_pp_extend")
+        return [(int(pair[0]), int(pair[1]))] if n else []
+
+    def truncate(self, seq: int, rows: int) -> None:
+        check(LIB.mr_pp_truncate(self.h, int(seq), int(rows)), "mr_pp_truncate")
+
+    def slide(self, seq: int, window: int, sinks: int = 0) -> int:
+        """Release the pages that no later query sees; returns how many."""
+        return self._count(LIB.mr_pp_slide(self.h, int(seq), int(window), int(sinks)), "mr_pp_slide")
+
+    def close(self, seq: int) -> None:
+        check(LIB.mr_pp_close(self.h, int(seq)), "mr_pp_close")
+
+    def compact(self, max_pairs: Optional[int] = None) -> np.ndarray:
+        """Move the pages in use to the front; returns the pairs [n][2] to copy."""
+        most = self.n_pages if max_pairs is None else int(max_pairs)
+        pairs = np.empty((max(0, most), 2), np.int32)
+        n = self._count(LIB.mr_pp_compact(self.h, pairs.ctypes.data, most), "mr_pp_compact")
+        return pairs[:n]
+
+    def rows(self, seq: int) -> int:
+        return self._table(seq, self.n_pages_of(seq))[1]
+
+    def n_pages_of(self, seq: int) -> int:
+        """Entries of the sequence's table."""
+        most = 64
+        while True:
+            buf = (_c_i32 * most)()
+            n = LIB.mr_pp_table(self.h, int(seq), buf, most, None)
+            if n != -MR_ERR_CAPACITY:
+                return self._count(n, "mr_pp_table")
+            most *= 4
+
+    def _table(self, seq: int, width: int):
+        pages, rows = np.empty(width, np.int32), ctypes.c_int(0)
+        self._count(LIB.mr_pp_table(self.h, int(seq), pages.ctypes.data, width, ctypes.byref(rows)), "mr_pp_table")
+        return pages, int(rows.value)
+
+    def tables(self, seqs, width: Optional[int] = None):
+        """Host arrays (table [n][width] int32, rows [n] int32) of some sequences, to copy to the device as
+        `table` and `kv_len`; entries without a page are -1."""
+        if width is None:
+            width = max([1] + [self.n_pages_of(s) for s in seqs])
+        got = [self._table(s, width) for s in seqs]
+        return np.stack([g[0] for g in got]), np.array([g[1] for g in got], np.int32)
+
+    def stats(self) -> dict:
+        v = (_c_i64 * 4)()
+        check(LIB.mr_pp_stats(self.h, v), "mr_pp_stats")
+        return dict(zip(("pages", "free", "sequences", "shared"), [int(x) for x in v]))

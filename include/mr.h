@@ -406,6 +406,199 @@ int mr_bm_evicted(mr_block_manager* bm, int64_t* ids, int max_ids);
 mr_status mr_bm_stats(mr_block_manager* bm, int64_t* out);
 
 /*
+ * ------------------------------------------------------------------------------------------------
+ * The receiver's paged key-value cache: rotary positions, appending new rows, attention of new rows
+ * over the cache (one token per sequence, or a chunk of rows), copying pages, and a host-side page
+ * pool.  MapFlow section 6 ("PagedAttention", "Chunked Prefill", variable-length packing): a
+ * receiver that reuses a prefix's maps still rotates and stores its own keys and values, computes
+ * the rows behind the prefix exactly, and then decodes token by token.
+ * ------------------------------------------------------------------------------------------------
+ *
+ * mr_rows: rows of a head-major tensor with explicit strides, in elements.  Element (h, row, c) is at
+ * ptr + h * head_stride + row * row_stride + c, so both [H][rows][d] and [rows][H][d] buffers fit.
+ * Strides must be >= 0; the heads and rows of an output must not overlap.
+ */
+typedef struct {
+  void* ptr;
+  int64_t head_stride;
+  int64_t row_stride;
+} mr_rows;
+
+/*
+ * A pool of pages, k and v each [n_pages][H_kv][page_rows][d] in dtype dt (the layout of
+ * mr_retrieve's v_pages, so one value pool serves both).  k and v must be 16-byte aligned.
+ * Supported: dt MR_BF16 or MR_F32; d in {64, 128}; H_kv >= 1; page_rows >= 1;
+ * n_pages * H_kv * page_rows < 2^31.  (mr_retrieve needs page_rows to be a multiple of 64.)
+ */
+typedef struct {
+  void* k;
+  void* v;
+  mr_dtype dt;
+  int32_t H_kv;
+  int32_t page_rows;
+  int32_t d;
+  int64_t n_pages;
+} mr_kv_cache;
+
+/*
+ * The sequences of a call.  table: device int32 [n_seq][pages_per_seq]; row j of sequence s is row
+ * j % page_rows of page table[s * pages_per_seq + j / page_rows].  kv_len: device int32 [n_seq], the
+ * rows each sequence holds, the call's new rows included.  With n new rows, new row i has position
+ * kv_len[s] - n + i.  Table entries behind the last row, and of pages whose rows are all outside the
+ * window (and not among the sinks), are not used.
+ * Conditions found on the device, all recorded as MR_ERR_DEVICE_CHECK: a used page number outside
+ * [0, n_pages) (its rows read as zeros and are not written); kv_len beyond pages_per_seq * page_rows
+ * (only the rows the table covers are read or written).  kv_len <= 0 is an empty sequence.
+ */
+typedef struct {
+  const int32_t* table;
+  const int32_t* kv_len;
+  int32_t pages_per_seq;
+  int32_t n_seq;
+} mr_kv_seqs;
+
+/*
+ * Rotary positions.  The first rot_dim of a row's d elements are rotated in pairs, the rest are
+ * copied: pair i (0 <= i < rot_dim / 2) is elements (i, i + rot_dim / 2), or (2i, 2i + 1) when
+ * interleaved, and position p turns it by the angle p * f_i:
+ *   y_a = mscale * (x_a cos(p f_i) - x_b sin(p f_i)),  y_b = mscale * (x_b cos(p f_i) + x_a sin(p f_i)).
+ * turn[i] holds f_i / (2 pi) as a 64-bit binary fraction of a turn, so p * turn[i] modulo 2^64 is the
+ * angle to 2^-32 turns at every 31-bit position.  Filled by mr_rope_init; plain data, copied freely.
+ */
+typedef struct {
+  int32_t d;
+  int32_t rot_dim;
+  int32_t interleaved;
+  float mscale;
+  uint64_t turn[128];
+} mr_rope;
+
+/*
+ * How f_i = base^(-2i / rot_dim) is changed for contexts longer than the model was trained on:
+ *   MR_ROPE_LINEAR  f_i / factor
+ *   MR_ROPE_BASE    base * factor^(rot_dim / (rot_dim - 2)) in place of base (rot_dim >= 4)
+ *   MR_ROPE_RAMP    g_i f_i + (1 - g_i) f_i / factor, g_i = clamp((r_i - beta_slow) /
+ *                   (beta_fast - beta_slow), 0, 1), r_i = orig_len f_i / (2 pi): pairs that turn more
+ *                   than beta_fast times over orig_len positions stay, those below beta_slow turns
+ *                   are stretched
+ */
+typedef enum { MR_ROPE_NONE = 0, MR_ROPE_LINEAR = 1, MR_ROPE_BASE = 2, MR_ROPE_RAMP = 3 } mr_rope_scaling;
+
+/*
+ * Fill *out (host).  d a positive multiple of 8, at most 256; rot_dim even, 2 <= rot_dim <= d; base > 1
+ * and finite; factor > 0 (1 for MR_ROPE_NONE); MR_ROPE_RAMP: orig_len >= 1, beta_fast > beta_slow >= 0;
+ * mscale finite.  inv_freq: NULL, or a host array of rot_dim / 2 finite angles per position in place
+ * of base and scaling.  Every |f_i| must be below 2 pi (one turn per position).
+ */
+mr_status mr_rope_init(mr_rope* out, int d, int rot_dim, int interleaved, double base,
+                       mr_rope_scaling scaling, double factor, int orig_len, double beta_slow,
+                       double beta_fast, double mscale, const double* inv_freq);
+
+/*
+ * Y = rotation of X (dtype dt, H heads x n_rows rows of rope->d elements) by each row's position
+ * pos[row] (device int32, 0 or more; a negative position turns the other way).  adjoint != 0 turns by
+ * the opposite angle with the same mscale: the gradient with respect to X given Y's.  X == Y with
+ * equal strides rotates in place; other overlaps are not allowed.  Arithmetic in fp32, one rounding
+ * to dt.  Needs no workspace: it has no device-side conditions.
+ */
+mr_status mr_rope_apply(const mr_rope* rope, const mr_rows* X, const mr_rows* Y, mr_dtype dt, int H,
+                        int n_rows, const int32_t* pos, int adjoint, void* stream);
+
+/* Workspace bytes of mr_kv_append, mr_paged_decode and mr_paged_attn for a cache, H_q query heads and
+ * n_seq sequences (device memory, 256-byte aligned).  0 for an unsupported shape. */
+size_t mr_paged_workspace_bytes(const mr_kv_cache* cache, int H_q, int n_seq);
+
+/*
+ * Append new rows to the cache: K rotated, V as it is, and rotate the queries into Q_out, in one
+ * launch.  All tensors in cache->dt; K, V have H_kv heads, Q and Q_out H_q heads, total_q rows.
+ *   rope   NULL: nothing is rotated (K copied; Q copied to Q_out).  Otherwise rope->d == cache->d.
+ *   Q, Q_out  both NULL, or both given (the same tensor rotates in place)
+ *   cu_q   device int32 [n_seq + 1] row offsets of each sequence in Q, K and V, ascending from 0, or
+ *          NULL when every sequence has one new row (total_q == n_seq)
+ *   total_q  host int, at least cu_q[n_seq]; rows at or behind cu_q[n_seq] are neither read nor
+ *          written (their Q_out rows stay as they were)
+ * A new row whose position is negative (kv_len[s] below its new rows) is not stored, its Q_out row is
+ * zero.  Sequences that share a page (after a fork) must not append into it: copy it first.
+ */
+mr_status mr_kv_append(const mr_kv_cache* cache, const mr_kv_seqs* seqs, const mr_rope* rope,
+                       const mr_rows* Q, const mr_rows* Q_out, int H_q, const mr_rows* K,
+                       const mr_rows* V, const int32_t* cu_q, int total_q, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/* Workspace bytes mr_pages_copy needs. */
+size_t mr_pages_copy_workspace_bytes(void);
+
+/*
+ * Copy pages: for every pair t, page pairs[2t + 1] <- page pairs[2t] in each of n_pools pools (the
+ * k and v pools of every layer), all pools of n_pages pages of page_bytes bytes.  For forking (the
+ * last page of a shared sequence before it is written) and for compacting a pool.
+ *   pools   host array of n_pools device pointers, 16-byte aligned
+ *   page_bytes  a positive multiple of 16
+ *   pairs   device int32 [n_pairs][2]: source, destination
+ * All pairs count as copied at once, so a pair is skipped and MR_ERR_DEVICE_CHECK recorded when its
+ * source or destination lies outside [0, n_pages), when its source is another pair's destination or when
+ * an earlier pair has the same destination.  A pair of a page with itself does nothing and counts for nothing.
+ * One source may go to many destinations.
+ */
+mr_status mr_pages_copy(void* const* pools, int n_pools, int64_t page_bytes, int64_t n_pages,
+                        const int32_t* pairs, int n_pairs, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Page pool: which pages of a pool each sequence holds (host only; thread-safe; touches no device
+ * memory).  Pages carry reference counts, so forked sequences share them until one of them writes.
+ * Calls that return pairs give (source, destination) page numbers for mr_pages_copy, to be copied before
+ * the pages are next read or written; until then the sources keep their content because the pool does
+ * not hand them out again before the next call.  Functions that return a count or id return
+ * -mr_status on an error, and change nothing then (MR_ERR_CAPACITY also when host memory runs out).
+ */
+typedef struct mr_page_pool mr_page_pool;
+
+/* New pool of n_pages free pages of page_rows rows.  NULL on bad arguments or without host memory. */
+mr_page_pool* mr_pp_create(int n_pages, int page_rows);
+void mr_pp_destroy(mr_page_pool* pp);
+
+/* New empty sequence: its id (>= 0). */
+int64_t mr_pp_open(mr_page_pool* pp);
+
+/* New sequence with the first `rows` rows of `seq`, sharing their pages: its id. */
+int64_t mr_pp_fork(mr_page_pool* pp, int64_t seq, int rows);
+
+/*
+ * Make room for `rows` more rows of `seq`: takes free pages, and for a shared page that the new rows
+ * would be written into a free page of its own.  Writes at most one pair to pair[2] (host int32) and
+ * returns the number of pairs (0 or 1).  -MR_ERR_CAPACITY when there are too few free pages.
+ */
+int mr_pp_extend(mr_page_pool* pp, int64_t seq, int rows, int32_t* pair);
+
+/* Drop the last rows of `seq` so that `rows` remain; pages without rows are released.  Refused (as a fork is)
+ * when the last row that would remain lies in a page given up by mr_pp_slide. */
+mr_status mr_pp_truncate(mr_page_pool* pp, int64_t seq, int rows);
+
+/*
+ * Release the pages of `seq` whose rows no later query sees under a window with sinks (window >= 1; the
+ * next query's position is at least the rows held).  Their table entries become -1.  Returns how
+ * many pages the sequence gave up.
+ */
+int mr_pp_slide(mr_page_pool* pp, int64_t seq, int window, int sinks);
+
+/* End a sequence: its pages lose a reference each. */
+mr_status mr_pp_close(mr_page_pool* pp, int64_t seq);
+
+/*
+ * Compact: renumber pages so that the pages in use are the first ones, and write the (source,
+ * destination) pairs to pairs (host int32 [max_pairs][2]).  Returns the number of pairs, at most
+ * max_pairs (the rest is left for a later call); sequences' tables change with it.
+ */
+int mr_pp_compact(mr_page_pool* pp, int32_t* pairs, int max_pairs);
+
+/* Write the page numbers of `seq` to pages (host int32 [max_pages], the rest filled with -1) and its
+ * rows to *rows (may be NULL).  Returns the sequence's page count; -MR_ERR_CAPACITY if max_pages is less. */
+int mr_pp_table(mr_page_pool* pp, int64_t seq, int32_t* pages, int max_pages, int* rows);
+
+/* out[4] = {pages, free pages, sequences, pages with more than one reference}. */
+mr_status mr_pp_stats(mr_page_pool* pp, int64_t* out);
+
+/*
  * Measurement hooks (not part of the method).  When profiling is enabled, every entry point
  * records a CUDA event on its stream before and after each kernel it launches; mr_profile_read
  * waits for the recorded events and reports, per kernel id, the summed elapsed milliseconds and
