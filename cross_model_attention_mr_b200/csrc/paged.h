@@ -52,6 +52,20 @@ struct RopeArgs {
   cudaStream_t stream;
 };
 
+struct DecodeArgs {
+  PagedKv kv;
+  mr_rows q, o;
+  int H_q;
+  mr_dtype dt;
+  float scale;
+  int window, sinks;
+  float* lse;
+  void* ws;  // decode_workspace_bytes: status header, join counters, partial results
+  cudaStream_t stream;
+};
+
+size_t decode_workspace_bytes(int d);
+cudaError_t launch_decode(const DecodeArgs& a);
 cudaError_t launch_rope(const RopeArgs& a);
 cudaError_t launch_append(const AppendArgs& a);
 cudaError_t launch_pages_copy(void* const* pools, int n_pools, int64_t page_bytes, int64_t n_pages,

@@ -107,6 +107,8 @@ EXPORTS = {
     "mr_kv_append": ([ctypes.POINTER(KvCache), ctypes.POINTER(KvSeqs), ctypes.POINTER(RopeTable), ctypes.POINTER(Rows),
                       ctypes.POINTER(Rows), ctypes.c_int, ctypes.POINTER(Rows), ctypes.POINTER(Rows), _c_p, ctypes.c_int,
                       _c_p, _c_sz, _c_p], ctypes.c_int),
+    "mr_paged_decode": ([ctypes.POINTER(KvCache), ctypes.POINTER(KvSeqs), ctypes.POINTER(Rows), ctypes.c_int, _c_f32,
+                         ctypes.c_int, ctypes.c_int, ctypes.POINTER(Rows), _c_p, _c_p, _c_sz, _c_p], ctypes.c_int),
     "mr_pages_copy_workspace_bytes": ([], _c_sz),
     "mr_pages_copy": ([ctypes.POINTER(_c_p), ctypes.c_int, _c_i64, _c_i64, _c_p, ctypes.c_int, _c_p, _c_sz, _c_p],
                       ctypes.c_int),
@@ -746,6 +748,45 @@ def kv_append(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, K: torc
                                _ints(cu_q, cache.k, "cu_q") if cu_q is not None else None, total, ws.ptr, ws.nbytes,
                                _stream(stream)), "mr_kv_append")
     return q_out
+
+
+def _attn_out(Q: torch.Tensor, out, lse, return_lse: bool):
+    """Output and log-normaliser tensors of an attention call on Q [H_q][rows][d]."""
+    H, n, d = Q.shape
+    if out is None:
+        out = torch.empty((H, n, d), dtype=Q.dtype, device=Q.device)
+    elif out.shape != Q.shape:
+        raise ValueError("out must have the shape of Q")
+    if lse is not None:
+        if lse.shape != (H, n) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != Q.device:
+            raise ValueError("lse must be a contiguous fp32 tensor [H_q][rows]")
+    elif return_lse:
+        lse = torch.empty((H, n), dtype=torch.float32, device=Q.device)
+    return out, lse
+
+
+def paged_decode(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, Q: torch.Tensor,
+                 scale: Optional[float] = None, window: int = 0, sinks: int = 0, out: Optional[torch.Tensor] = None,
+                 lse: Optional[torch.Tensor] = None, return_lse: bool = False, ws: Optional[Workspace] = None,
+                 stream=None):
+    """mr_paged_decode: attention of one new token per sequence, Q [H_q][n_seq][d], over the kv_len [n_seq]
+    rows that table [n_seq][pages_per_seq] names -> O [H_q][n_seq][d], or (O, lse [H_q][n_seq]) with
+    ``return_lse`` or an ``lse`` tensor.  ``window`` rows back and the first ``sinks`` rows are visible
+    (window 0: all)."""
+    with _on_device_of(cache.k):
+        q = _rows(Q, cache.k, "Q")
+        seqs = _seqs(cache, table, kv_len)
+        H = Q.shape[0]
+        if Q.shape[1] != seqs.n_seq or Q.shape[2] != cache.d:
+            raise ValueError("Q must be [H_q][n_seq][d]")
+        out, lse = _attn_out(Q, out, lse, return_lse)
+        if ws is None:
+            ws = Workspace(paged_workspace_bytes(cache, H, seqs.n_seq), cache.k.device)
+        check(LIB.mr_paged_decode(ctypes.byref(cache.c), ctypes.byref(seqs), ctypes.byref(q), H,
+                                  1.0 / math.sqrt(cache.d) if scale is None else float(scale), int(window), int(sinks),
+                                  ctypes.byref(_rows(out, cache.k, "out")), lse.data_ptr() if lse is not None else None,
+                                  ws.ptr, ws.nbytes, _stream(stream)), "mr_paged_decode")
+    return out if lse is None else (out, lse)
 
 
 def pages_copy_workspace_bytes() -> int:

@@ -525,6 +525,25 @@ mr_status mr_kv_append(const mr_kv_cache* cache, const mr_kv_seqs* seqs, const m
                        const mr_rows* V, const int32_t* cu_q, int total_q, void* ws, size_t ws_bytes,
                        void* stream);
 
+/*
+ * Which rows a query at position p sees: row j when 0 <= j <= p and (window == 0, or j > p - window,
+ * or j < sinks).  window 0: every earlier row.  sinks: first rows that stay visible outside the window.
+ */
+
+/*
+ * Attention of one new token per sequence over its cached rows (its own included):
+ *   O_h = sum_j softmax_j(scale * q_h.k_j) v_j over the rows j visible from position kv_len[s] - 1,
+ * query head h reading key-value head h / (H_q / H_kv).  Q, O: H_q heads, row s for sequence s.
+ *   lse  NULL or device fp32 [H_q][n_seq]: natural log of sum_j exp(scale * q.k_j)
+ * A sequence without visible rows gets O = 0 and lse = -inf.  Rows that are not visible, stale rows of
+ * the last page among them, do not influence the result whatever they hold (infinities and NaN too).
+ * H_q must be a multiple of H_kv.  Work is split along every sequence's length over the whole GPU
+ * and joined in a fixed order: results do not vary from call to call.
+ */
+mr_status mr_paged_decode(const mr_kv_cache* cache, const mr_kv_seqs* seqs, const mr_rows* Q, int H_q,
+                          float scale, int window, int sinks, const mr_rows* O, float* lse, void* ws,
+                          size_t ws_bytes, void* stream);
+
 /* Workspace bytes mr_pages_copy needs. */
 size_t mr_pages_copy_workspace_bytes(void);
 
