@@ -1,0 +1,364 @@
+// Attention of a chunk of new rows per sequence over the paged cache, on the CUDA cores: fp32, and the bf16 calls whose
+// alignment or page size the tensor-core kernel does not take.
+//
+// Bound by fp32 arithmetic: 4 d operations for a row and a key it sees.  A CTA holds a tile of 64 query rows (rows
+// x the query heads that share a key head, so a tile of keys serves all of them) and walks key tiles of 64.  16 x 16
+// threads own 4 x 4 scores and 4 x d/16 outputs each: 64 multiply-adds for 8 16-byte reads of shared memory.  Scores
+// are turned into probabilities with a running maximum and sum per row, held by the 16 threads of the row.
+#include <cuda_bf16.h>
+
+#include "attn_units.cuh"
+#include "profile.h"
+#include "sm100.cuh"
+
+namespace mr {
+namespace {
+
+using sm100::ex2_approx;
+using sm100::smem_u32;
+
+constexpr int kThreads = 256;
+constexpr int kRows = 64;   // query rows of a unit
+constexpr int kKeys = 64;   // keys of a tile
+constexpr int kMaxHeads = 32;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D>
+struct Smem {
+  static constexpr int kStride = D + 4;       // floats; shifts rows by 16 bytes in the banks
+  static constexpr int kPStride = kKeys + 4;
+  float q[kRows * kStride];
+  float k[kKeys * kStride];                   // the probabilities take its place
+  float v[kKeys * D];
+  PartitionSmem part;
+  int last;
+};
+static_assert(Smem<64>::kPStride * kRows <= kKeys * Smem<64>::kStride, "probabilities fit");
+
+// `live` rows of K or V from the pool into shared memory as fp32; the others become zeros.
+template <typename T, int D>
+__device__ __forceinline__ void load_rows(const AttnParams& p, const Seg& sg, const void* pool, int key0, int lo, int hi,
+                                          float* dst, int stride) {
+  constexpr int V = 16 / sizeof(T);            // elements of a 16-byte load
+  constexpr int kVecs = kKeys * (D / V);
+#pragma unroll 4
+  for (int e = threadIdx.x; e < kVecs; e += kThreads) {
+    const int r = e / (D / V), c = (e % (D / V)) * V;
+    const int j = key0 + r;
+    float* d = dst + r * stride + c;
+    int row = -1;
+    if (j <= hi && (j >= lo || j < p.sinks)) {
+      row = pool_row(p.kv, sg.u.s, sg.g, j);
+      if (row < 0) set_status(p.ws, MR_ERR_DEVICE_CHECK, kBadPage);
+    }
+    const T* src = (const T*)pool + (int64_t)max(row, 0) * D + c;
+    if constexpr (sizeof(T) == 4) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(d)), "l"(src), "r"(row >= 0 ? 16 : 0)
+                   : "memory");
+    } else {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (row >= 0) x = *reinterpret_cast<const uint4*>(src);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; i += 2)
+        *reinterpret_cast<float4*>(d + 2 * i) =
+            make_float4(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u),
+                        __uint_as_float(w[i + 1] << 16), __uint_as_float(w[i + 1] & 0xffff0000u));
+    }
+  }
+}
+
+template <int D, bool Edge>
+__device__ __forceinline__ void product(const float* pr, const float* v, float (&acc)[4][D / 16]) {
+  // pr: this thread's 4 rows of probabilities (a masked one is -1), v: its columns 4 tx + 64 c
+#pragma unroll 2
+  for (int j = 0; j < kKeys; j += 4) {
+    float4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(pr + i * Smem<D>::kPStride + j);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const float4 x = *reinterpret_cast<const float4*>(v + (j + e) * D + 64 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float y = e == 0 ? w[i].x : e == 1 ? w[i].y : e == 2 ? w[i].z : w[i].w;
+          if (!Edge || !(y < 0.f)) {  // what a masked row holds, infinities and NaN included, must not count
+            acc[i][4 * c] = fmaf(y, x.x, acc[i][4 * c]);
+            acc[i][4 * c + 1] = fmaf(y, x.y, acc[i][4 * c + 1]);
+            acc[i][4 * c + 2] = fmaf(y, x.z, acc[i][4 * c + 2]);
+            acc[i][4 * c + 3] = fmaf(y, x.w, acc[i][4 * c + 3]);
+          }
+        }
+      }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(const AttnParams& p, int64_t at, float4 x) {
+  T* o = (T*)p.o + at;
+  if (sizeof(T) == 4 && p.vec_o) {
+    *reinterpret_cast<float4*>(o) = x;
+  } else {
+    o[0] = from_f32<T>(x.x);
+    o[1] = from_f32<T>(x.y);
+    o[2] = from_f32<T>(x.z);
+    o[3] = from_f32<T>(x.w);
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 2) k_attn(const AttnParams p) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  Smem<D>& s = *reinterpret_cast<Smem<D>*>(smem_raw);
+  constexpr int kStride = Smem<D>::kStride, kPStride = Smem<D>::kPStride;
+  constexpr int kSlot = kRows * (D + 2);  // floats of a part: 64 (maximum, sum), then outputs
+  empty_rows<T, D, kThreads>(p);
+  Share sh;
+  if (!make_share<kKeys, kThreads>(p, s.part, sh)) return;
+  Segments<kKeys> walk(p, sh);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  Seg sg;
+  while (walk.next(sg)) {
+    const Unit& u = sg.u;
+    // query rows: head r / tile_tokens, new row r % tile_tokens
+    for (int e = threadIdx.x; e < kRows * D; e += kThreads) {
+      const int r = e / D, c = e % D;
+      const int hh = (int)fast_div((uint32_t)r, p.by_tile_tokens), t = r - hh * p.tile_tokens;
+      s.q[r * kStride + c] =
+          hh < sg.heads && t < u.n
+              ? to_f32<T>(((const T*)p.q)[(int64_t)(sg.h0 + hh) * p.q_head + (int64_t)(u.q0 + t) * p.q_row + c])
+              : 0.f;
+    }
+    int hh[4], tok[4], pos[4], last[4];  // of this thread's rows: head, new row (-1: none), position, last row seen
+    float m[4], l[4], acc[4][D / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * ty + i;
+      hh[i] = (int)fast_div((uint32_t)r, p.by_tile_tokens);
+      tok[i] = r - hh[i] * p.tile_tokens;
+      if (hh[i] >= sg.heads || tok[i] >= u.n) tok[i] = -1;
+      pos[i] = u.pos0 + max(tok[i], 0);
+      last[i] = tok[i] < 0 ? -1 : min(pos[i], u.held - 1);
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+    }
+    const int hi = min(u.pos0 + u.n - 1, u.held - 1);
+    const int lo = p.window > 0 && u.pos0 >= p.window ? u.pos0 - p.window + 1 : 0;
+    const int pos_last = u.pos0 + u.n - 1;
+    for (int j = sg.j0; j < sg.j1; ++j) {
+      const int key0 = tile_of(u, j) * kKeys;
+      load_rows<T, D>(p, sg, p.kv.k, key0, lo, hi, s.k, kStride);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      load_rows<T, D>(p, sg, p.kv.v, key0, lo, hi, s.v, D);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncthreads();
+      float x[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) x[i][n] = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < D; c += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(s.q + (4 * ty + i) * kStride + c);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) b[n] = *reinterpret_cast<const float4*>(s.k + (tx + 16 * n) * kStride + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            x[i][n] = fmaf(a[i].x, b[n].x, x[i][n]);
+            x[i][n] = fmaf(a[i].y, b[n].y, x[i][n]);
+            x[i][n] = fmaf(a[i].z, b[n].z, x[i][n]);
+            x[i][n] = fmaf(a[i].w, b[n].w, x[i][n]);
+          }
+      }
+      // some row of the tile may not see some key (pos0 < 0 included)
+      const bool edge = key0 + kKeys - 1 > min(u.pos0, u.held - 1) ||
+                        (p.window > 0 && pos_last >= p.window && key0 <= pos_last - p.window && key0 + kKeys > p.sinks);
+      float f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int key = key0 + tx + 16 * n;
+          const bool seen = !edge || (key <= last[i] && (p.window == 0 || key > pos[i] - p.window || key < p.sinks));
+          x[i][n] = seen ? x[i][n] * p.a : -INFINITY;
+          mx = fmaxf(mx, x[i][n]);
+        }
+#pragma unroll
+        for (int w = 1; w < 16; w *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+        f[i] = 1.f;
+        if (mx > m[i]) {
+          f[i] = ex2_approx(m[i] - mx);
+          m[i] = mx;
+        }
+        const float ref = m[i] == -INFINITY ? 0.f : m[i];
+        l[i] *= f[i];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int key = key0 + tx + 16 * n;
+          const bool seen = !edge || (key <= last[i] && (p.window == 0 || key > pos[i] - p.window || key < p.sinks));
+          const float y = ex2_approx(x[i][n] - ref);
+          x[i][n] = seen ? y : -1.f;
+          l[i] += seen ? y : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) acc[i][c] *= f[i];
+      }
+      __syncthreads();  // every thread has read the keys
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) s.k[(4 * ty + i) * kPStride + tx + 16 * n] = x[i][n];
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();
+      if (edge)
+        product<D, true>(s.k + 4 * ty * kPStride, s.v + 4 * tx, acc);
+      else
+        product<D, false>(s.k + 4 * ty * kPStride, s.v + 4 * tx, acc);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int w = 1; w < 16; w *= 2) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+
+    bool finish = sg.whole();
+    if (!finish) {
+      int first, lastc;
+      holders(sh, sg, first, lastc);
+      float* mine = p.part + slot_of(blockIdx.x, first) * kSlot;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+        if (tx == 0) __stcg(reinterpret_cast<float2*>(mine) + r, make_float2(m[i], l[i]));
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          __stcg(reinterpret_cast<float4*>(mine + 2 * kRows + r * D + 4 * tx + 64 * c),
+                 make_float4(acc[i][4 * c], acc[i][4 * c + 1], acc[i][4 * c + 2], acc[i][4 * c + 3]));
+      }
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) s.last = atomicAdd(p.counters + first, 1u) == (uint32_t)(lastc - first);
+      __syncthreads();
+      finish = s.last != 0;
+      if (finish) {
+        __threadfence();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 4 * ty + i;
+          m[i] = -INFINITY;
+          for (int c = first; c <= lastc; ++c)
+            m[i] = fmaxf(m[i], __ldcg(reinterpret_cast<const float2*>(p.part + slot_of(c, first) * kSlot) + r).x);
+          const float ref = m[i] == -INFINITY ? 0.f : m[i];
+          l[i] = 0.f;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+          for (int b = first; b <= lastc; ++b) {
+            const float* part = p.part + slot_of(b, first) * kSlot;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part) + r);
+            const float w = ex2_approx(ml.x - ref);
+            l[i] = fmaf(w, ml.y, l[i]);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+              const float4 y = __ldcg(reinterpret_cast<const float4*>(part + 2 * kRows + r * D + 4 * tx + 64 * c));
+              acc[i][4 * c] = fmaf(w, y.x, acc[i][4 * c]);
+              acc[i][4 * c + 1] = fmaf(w, y.y, acc[i][4 * c + 1]);
+              acc[i][4 * c + 2] = fmaf(w, y.z, acc[i][4 * c + 2]);
+              acc[i][4 * c + 3] = fmaf(w, y.w, acc[i][4 * c + 3]);
+            }
+          }
+        }
+      }
+    }
+    if (finish) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (tok[i] < 0) continue;
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        const int h = sg.h0 + hh[i], row = u.q0 + tok[i];
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          store4<T>(p, (int64_t)h * p.o_head + (int64_t)row * p.o_row + 4 * tx + 64 * c,
+                    make_float4(acc[i][4 * c] * inv, acc[i][4 * c + 1] * inv, acc[i][4 * c + 2] * inv,
+                                acc[i][4 * c + 3] * inv));
+        if (tx == 0 && p.lse)
+          p.lse[(int64_t)h * p.total_q + row] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+      }
+    }
+    __syncthreads();  // shared memory is free again
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
+  constexpr int smem = (int)sizeof(Smem<D>);
+  cudaError_t e = cudaFuncSetAttribute(k_attn<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = 2 * sms < kAttnMaxCtas ? 2 * sms : kAttnMaxCtas;
+  ProfScope ps(kKAttn, st);
+  k_attn<T, D><<<grid, kThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+constexpr size_t kCounterBytes = (kAttnMaxCtas * sizeof(uint32_t) + 255) / 256 * 256;
+
+}  // namespace
+
+size_t attn_workspace_bytes(int d) {
+  return kWsHeaderBytes + kCounterBytes + (size_t)2 * kAttnMaxCtas * kRows * (d + 2) * sizeof(float);
+}
+
+void attn_split(AttnParams& p, int rows, int max_heads) {
+  p.chunks = (p.group + max_heads - 1) / max_heads;
+  p.hp = (p.group + p.chunks - 1) / p.chunks;
+  p.tile_tokens = rows / p.hp;
+  p.by_tile_tokens = make_fastdiv((uint32_t)p.tile_tokens);
+}
+
+cudaError_t launch_attn(const AttnArgs& a) {
+  int dev = 0, sms = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  if ((e = cudaMemsetAsync(a.ws, 0, kWsHeaderBytes + kCounterBytes, a.stream)) != cudaSuccess) return e;
+  if (a.total_q == 0) return cudaSuccess;
+  AttnParams p{};
+  p.kv = a.kv;
+  p.q = a.q.ptr;
+  p.o = a.o.ptr;
+  p.q_head = a.q.head_stride;
+  p.q_row = a.q.row_stride;
+  p.o_head = a.o.head_stride;
+  p.o_row = a.o.row_stride;
+  p.lse = a.lse;
+  p.cu = a.cu_q;
+  p.total_q = a.total_q;
+  p.H_q = a.H_q;
+  p.group = a.H_q / a.kv.H_kv;
+  const int es = a.dt == MR_BF16 ? 2 : 4;
+  p.vec_q = ((uintptr_t)a.q.ptr | (uintptr_t)(a.q.head_stride * es) | (uintptr_t)(a.q.row_stride * es)) % 16 == 0;
+  p.vec_o = ((uintptr_t)a.o.ptr | (uintptr_t)(a.o.head_stride * es) | (uintptr_t)(a.o.row_stride * es)) % 16 == 0;
+  p.a = a.scale * 1.4426950408889634f;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.ws = (WsHeader*)a.ws;
+  p.counters = (uint32_t*)((char*)a.ws + kWsHeaderBytes);
+  p.part = (float*)((char*)a.ws + kWsHeaderBytes + kCounterBytes);
+  attn_split(p, kRows, kMaxHeads);
+  p.tokens = p.tile_tokens;
+  p.min_steps = 2;
+  if (a.dt == MR_BF16)
+    return a.kv.d == 64 ? launch<__nv_bfloat16, 64>(p, sms, a.stream) : launch<__nv_bfloat16, 128>(p, sms, a.stream);
+  return a.kv.d == 64 ? launch<float, 64>(p, sms, a.stream) : launch<float, 128>(p, sms, a.stream);
+}
+
+}  // namespace mr

@@ -64,6 +64,27 @@ struct DecodeArgs {
   cudaStream_t stream;
 };
 
+struct AttnArgs {
+  PagedKv kv;
+  mr_rows q, o;
+  int H_q;
+  mr_dtype dt;
+  const int32_t* cu_q;
+  int total_q;
+  float scale;
+  int window, sinks;
+  float* lse;
+  void* ws;  // attn_workspace_bytes: status header, join counters, partial results
+  cudaStream_t stream;
+};
+
+struct AttnParams;
+constexpr int kAttnMaxCtas = 304;  // two per SM (148) at most; sizes counters and partial results
+
+size_t attn_workspace_bytes(int d);
+// chunks of at most max_heads query heads, and the new rows that a tile of `rows` query rows takes of each
+void attn_split(AttnParams& p, int rows, int max_heads);
+cudaError_t launch_attn(const AttnArgs& a);
 size_t decode_workspace_bytes(int d);
 cudaError_t launch_decode(const DecodeArgs& a);
 cudaError_t launch_rope(const RopeArgs& a);

@@ -101,7 +101,8 @@ mr_status mr_rope_apply(const mr_rope* rope, const mr_rows* X, const mr_rows* Y,
 
 size_t mr_paged_workspace_bytes(const mr_kv_cache* cache, int H_q, int n_seq) {
   if (cache_ok(cache) != MR_OK || H_q < 1 || H_q > kMaxHeads || H_q % cache->H_kv || n_seq < 1) return 0;
-  return decode_workspace_bytes(cache->d);
+  const size_t dec = decode_workspace_bytes(cache->d), att = attn_workspace_bytes(cache->d);
+  return dec > att ? dec : att;
 }
 
 mr_status mr_kv_append(const mr_kv_cache* cache, const mr_kv_seqs* seqs, const mr_rope* rope,
@@ -172,6 +173,36 @@ mr_status mr_paged_decode(const mr_kv_cache* cache, const mr_kv_seqs* seqs, cons
   a.ws = ws;
   a.stream = (cudaStream_t)stream;
   return from_cuda(launch_decode(a));
+}
+
+mr_status mr_paged_attn(const mr_kv_cache* cache, const mr_kv_seqs* seqs, const mr_rows* Q, int H_q,
+                        const int32_t* cu_q, int total_q, float scale, int window, int sinks,
+                        const mr_rows* O, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  mr_status e;
+  if ((e = cache_ok(cache)) != MR_OK || (e = pools_ok(cache)) != MR_OK || (e = seqs_ok(seqs)) != MR_OK) return e;
+  if (H_q < 1 || H_q % cache->H_kv || window < 0 || sinks < 0 || !isfinite(scale)) return MR_ERR_INVALID_ARG;
+  if (H_q > kMaxHeads) return MR_ERR_UNSUPPORTED;
+  if (!cu_q || total_q < 0) return MR_ERR_INVALID_ARG;
+  const int es = esize(cache->dt), d = cache->d;
+  if (total_q > 0 && (!rows_ok(Q, H_q, total_q, d, es, false) || !rows_ok(O, H_q, total_q, d, es, true)))
+    return MR_ERR_INVALID_ARG;
+  if (!ws || ((uintptr_t)ws & 15u) || ws_bytes < mr_paged_workspace_bytes(cache, H_q, seqs->n_seq))
+    return MR_ERR_INVALID_ARG;
+  AttnArgs a;
+  a.kv = view(cache, seqs);
+  a.q = total_q > 0 ? *Q : mr_rows{};
+  a.o = total_q > 0 ? *O : mr_rows{};
+  a.H_q = H_q;
+  a.dt = cache->dt;
+  a.cu_q = cu_q;
+  a.total_q = total_q;
+  a.scale = scale;
+  a.window = window;
+  a.sinks = sinks;
+  a.lse = lse;
+  a.ws = ws;
+  a.stream = (cudaStream_t)stream;
+  return from_cuda(launch_attn(a));
 }
 
 size_t mr_pages_copy_workspace_bytes(void) { return kWsHeaderBytes; }

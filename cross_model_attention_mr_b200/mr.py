@@ -109,6 +109,9 @@ EXPORTS = {
                       _c_p, _c_sz, _c_p], ctypes.c_int),
     "mr_paged_decode": ([ctypes.POINTER(KvCache), ctypes.POINTER(KvSeqs), ctypes.POINTER(Rows), ctypes.c_int, _c_f32,
                          ctypes.c_int, ctypes.c_int, ctypes.POINTER(Rows), _c_p, _c_p, _c_sz, _c_p], ctypes.c_int),
+    "mr_paged_attn": ([ctypes.POINTER(KvCache), ctypes.POINTER(KvSeqs), ctypes.POINTER(Rows), ctypes.c_int, _c_p,
+                       ctypes.c_int, _c_f32, ctypes.c_int, ctypes.c_int, ctypes.POINTER(Rows), _c_p, _c_p, _c_sz, _c_p],
+                      ctypes.c_int),
     "mr_pages_copy_workspace_bytes": ([], _c_sz),
     "mr_pages_copy": ([ctypes.POINTER(_c_p), ctypes.c_int, _c_i64, _c_i64, _c_p, ctypes.c_int, _c_p, _c_sz, _c_p],
                       ctypes.c_int),
@@ -786,6 +789,31 @@ def paged_decode(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, Q: t
                                   1.0 / math.sqrt(cache.d) if scale is None else float(scale), int(window), int(sinks),
                                   ctypes.byref(_rows(out, cache.k, "out")), lse.data_ptr() if lse is not None else None,
                                   ws.ptr, ws.nbytes, _stream(stream)), "mr_paged_decode")
+    return out if lse is None else (out, lse)
+
+
+def paged_attn(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, Q: torch.Tensor, cu_q: torch.Tensor,
+               scale: Optional[float] = None, window: int = 0, sinks: int = 0, out: Optional[torch.Tensor] = None,
+               lse: Optional[torch.Tensor] = None, return_lse: bool = False, ws: Optional[Workspace] = None, stream=None):
+    """mr_paged_attn: causal attention of the new rows Q [H_q][total_q][d] (rows cu_q[s] .. cu_q[s + 1] - 1 are the
+    last ones of sequence s) over the cache -> O [H_q][total_q][d], or (O, lse [H_q][total_q]).  The rows' own keys
+    and values must be in the cache (kv_append).  Rows behind cu_q[n_seq] are left as they are."""
+    with _on_device_of(cache.k):
+        q = _rows(Q, cache.k, "Q")
+        seqs = _seqs(cache, table, kv_len)
+        H, total = Q.shape[:2]
+        if Q.shape[2] != cache.d:
+            raise ValueError("Q must be [H_q][total_q][d] of the cache")
+        if cu_q.shape[0] != seqs.n_seq + 1:
+            raise ValueError("cu_q must have n_seq + 1 entries")
+        out, lse = _attn_out(Q, out, lse, return_lse)
+        if ws is None:
+            ws = Workspace(paged_workspace_bytes(cache, H, seqs.n_seq), cache.k.device)
+        check(LIB.mr_paged_attn(ctypes.byref(cache.c), ctypes.byref(seqs), ctypes.byref(q), H,
+                                _ints(cu_q, cache.k, "cu_q"), total,
+                                1.0 / math.sqrt(cache.d) if scale is None else float(scale), int(window), int(sinks),
+                                ctypes.byref(_rows(out, cache.k, "out")), lse.data_ptr() if lse is not None else None,
+                                ws.ptr, ws.nbytes, _stream(stream)), "mr_paged_attn")
     return out if lse is None else (out, lse)
 
 

@@ -544,6 +544,20 @@ mr_status mr_paged_decode(const mr_kv_cache* cache, const mr_kv_seqs* seqs, cons
                           float scale, int window, int sinks, const mr_rows* O, float* lse, void* ws,
                           size_t ws_bytes, void* stream);
 
+/*
+ * The same for a chunk of new rows per sequence (a prompt, or the rows behind a reused prefix), whose
+ * keys and values are in the cache already.  cu_q: device int32 [n_seq + 1], ascending from 0; rows
+ * cu_q[s] .. cu_q[s + 1] - 1 of Q and O belong to sequence s and have the positions kv_len[s] - n ..
+ * kv_len[s] - 1.  total_q >= cu_q[n_seq]; rows of O and lse at or behind cu_q[n_seq] stay as they were.
+ *   lse  NULL or device fp32 [H_q][total_q]
+ * A row that sees nothing (a negative position) gets O = 0 and lse = -inf.  Rows of the cache that a new
+ * row does not see do not influence its result, whatever they hold.  Probabilities enter the second
+ * product in the cache's type (bf16: off by at most 2^-8 of themselves); sums are fp32.
+ */
+mr_status mr_paged_attn(const mr_kv_cache* cache, const mr_kv_seqs* seqs, const mr_rows* Q, int H_q,
+                        const int32_t* cu_q, int total_q, float scale, int window, int sinks,
+                        const mr_rows* O, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* Workspace bytes mr_pages_copy needs. */
 size_t mr_pages_copy_workspace_bytes(void);
 

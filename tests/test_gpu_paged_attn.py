@@ -10,8 +10,10 @@ from paged_ref import attend, attend_tol
 pytestmark = pytest.mark.gpu
 
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
-# half a step of the probabilities in the second product: two bf16 parts (2^-9 of 2^-9), or fp32
-DECODE_P = {"bf16": 2.0 ** -17, "f32": 0.0}
+# half a step of the probabilities in the second product: two bf16 parts (2^-8 of 2^-8), or fp32
+DECODE_P = {"bf16": 2.0 ** -16, "f32": 0.0}
+# one bf16 part, or fp32
+ATTN_P = {"bf16": 2.0 ** -8, "f32": 0.0}
 
 
 @pytest.fixture(scope="module")
@@ -199,3 +201,184 @@ def test_decode_on_a_stream_and_in_a_graph(mr):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, mr.paged_decode(cache, table, lens, q))
+
+
+# ---------------------------------------------------------------------------------------------- chunks of new rows
+# new rows and rows held of each sequence, H_q, H_kv, page_rows, d
+CHUNKS = [
+    ([1], [1], 1, 1, 16, 64), ([3, 0, 5], [3, 9, 200], 4, 2, 16, 128), ([70, 1, 200], [70, 333, 230], 8, 2, 64, 128),
+    ([33], [300], 7, 1, 7, 64), ([130, 129], [130, 700], 5, 5, 32, 64), ([257], [400], 28, 4, 128, 128),
+    ([20, 20], [15, 20], 2, 1, 16, 64), ([5, 3], [0, -4], 2, 2, 16, 128), ([100], [1000], 40, 1, 48, 128),
+    ([2], [3000], 3, 1, 16, 64), ([1, 1, 1], [513, 1, 64], 66, 2, 8, 64), ([300], [300], 1, 1, 1, 128),
+    ([384], [512], 1, 1, 128, 128), ([9] * 20, [40 + i for i in range(20)], 8, 4, 16, 64),
+]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("case", range(len(CHUNKS)))
+def test_attn_against_64_bits(mr, dt, case):
+    new, held, Hq, Hk, pr, d = CHUNKS[case]
+    c = Case(mr, new, held, Hq, Hk, pr, d, dt, seed=case, behind=3)
+    cache, table, lens, q = c.args()
+    O = torch.full_like(q, 5.0)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    mr.paged_attn(cache, table, lens, q, c.cu, out=O, lse=lse, ws=c.ws)
+    c.check(O, lse, p_eps=ATTN_P[dt])
+    assert bool((O[:, c.T:] == 5.0).all()) and bool((lse[:, c.T:] == 7.0).all())
+    again, lse2 = mr.paged_attn(cache, table, lens, q, c.cu, return_lse=True, ws=c.ws)
+    assert torch.equal(O[:, : c.T], again[:, : c.T]) and torch.equal(lse[:, : c.T], lse2[:, : c.T])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("pr", [16, 12])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (40, 0), (64, 16), (100, 200), (5000, 16), (0, 16), (130, 129),
+                                          (17, 1000), (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_attn_window_and_sinks(mr, dt, pr, window, sinks):
+    c = Case(mr, [300, 1, 18, 150], [300, 400, 700, 129], 8, 2, pr, 64, dt, seed=3)
+    c.hide(window, sinks)
+    O, lse = mr.paged_attn(*c.args(), c.cu, window=window, sinks=sinks, return_lse=True, ws=c.ws)
+    c.check(O, lse, window=window, sinks=sinks, p_eps=ATTN_P[dt])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale,spread", [(0.0, 1.0), (-0.3, 1.0), (2.0, 8.0)])
+def test_attn_scales(mr, dt, d, scale, spread):
+    c = Case(mr, [70, 90], [500, 90], 6, 2, 32, d, dt, seed=4, spread=spread)
+    O, lse = mr.paged_attn(*c.args(), c.cu, scale=scale, return_lse=True, ws=c.ws)
+    c.check(O, lse, scale=scale, p_eps=ATTN_P[dt])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_attn_growing_logits(mr, dt):
+    """Scores that keep passing the running maximum, so that what was summed has to be scaled again and again."""
+    c = Case(mr, [40], [900], 2, 1, 16, 128, dt, seed=5)
+    ramp = (torch.arange(900, dtype=torch.float32) / 60).to(DT[dt]).cuda()
+    c.q[:, :, 0] = 4.0
+    for j in range(900):
+        c.k[c.table[0, j // 16], 0, j % 16, 0] = ramp[j]
+        c.clean_k[int(c.table[0, j // 16]), 0, j % 16, 0] = float(ramp[j])
+    O, lse = mr.paged_attn(*c.args(), c.cu, scale=2.0, return_lse=True, ws=c.ws)
+    c.check(O, lse, scale=2.0, p_eps=ATTN_P[dt])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attn_many_units_and_parts(mr, dt, d):
+    c = Case(mr, [700, 1, 90, 0, 350], [700, 2500, 1400, 30, 3600], 4, 2, 64, d, dt, seed=6)
+    O, lse = mr.paged_attn(*c.args(), c.cu, window=1000, sinks=20, return_lse=True, ws=c.ws)
+    c.check(O, lse, window=1000, sinks=20, p_eps=ATTN_P[dt])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_attn_rows_that_only_some_see(mr, dt, what, bad):
+    """A value that is not finite, in a row that is the future of some new rows and outside the window of others, reaches
+    the rows that see it and no other."""
+    c = Case(mr, [200, 60], [260, 60], 4, 2, 16, 128, dt, seed=7)
+    cache, table, lens, q = c.args()
+    want, wl = mr.paged_attn(cache, table, lens, q, c.cu, window=64, sinks=4, return_lse=True)
+    row = 130                                              # new rows 70 .. 133 of sequence 0 see it
+    getattr(c, what)[c.table[0, row // 16], 1, row % 16, 11] = bad
+    got, gl = mr.paged_attn(cache, table, lens, q, c.cu, window=64, sinks=4, return_lse=True, ws=c.ws)
+    seen = torch.zeros(4, 260, dtype=torch.bool, device="cuda")
+    seen[2:, 70: 134] = True
+    # rows that are computed another way once such a value is found may differ by roundings: half a step of the
+    # probabilities and of the output each
+    tol = (torch.finfo(DT[dt]).eps + 2.0 ** -18) * c.v.float().nan_to_num(0, 0, 0).abs().max()
+    assert bool(((got - want)[~seen].abs() <= tol).all())
+    assert bool(((gl - wl)[~seen].abs() <= 1e-5).all())
+    if what == "v":
+        assert bool(((gl - wl).abs() <= 1e-5).all())
+        rest = torch.ones(128, dtype=torch.bool)
+        rest[11] = False
+        assert bool(((got - want)[seen][:, rest].abs() <= tol).all())
+        assert bool((~torch.isfinite(got[seen][:, 11])).all())
+    elif math.isnan(bad):
+        assert bool(torch.isnan(got[seen]).all()) and bool(torch.isnan(gl[seen]).all())
+    else:                                                  # scores of +inf (NaN) and -inf (nothing: like hidden)
+        up = seen & (q[:, :, 11] > 0)
+        assert bool(torch.isnan(got[up]).all()) and bool(torch.isfinite(got[seen & (q[:, :, 11] < 0)]).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_attn_strides_and_alignment(mr, dt):
+    c = Case(mr, [40, 3], [50, 120], 6, 2, 16, 64, dt, seed=8)
+    cache, table, lens, q = c.args()
+    want, _, A, S = attend(np64(q), c.clean_k, c.clean_v, c.table.numpy(), c.lens.numpy(), c.new, 0.125)
+    tol = attend_tol(want, _, A, S, 64, 120, torch.finfo(DT[dt]).eps, ATTN_P[dt])[0]
+    for width, off in ((64, 0), (72, 8), (67, 1)):               # [rows][heads][width] storage
+        buf = torch.full((43 * 6 * width + off,), 5.0, dtype=q.dtype, device="cuda")
+        out = buf[off:].view(43, 6, width).transpose(0, 1)[..., :64]
+        qv = torch.empty_like(buf)[off:].view(43, 6, width).transpose(0, 1)[..., :64]
+        qv.copy_(q)
+        mr.paged_attn(cache, table, lens, qv, c.cu, out=out, ws=c.ws)
+        assert np.all(np.abs(np64(out) - want) <= tol)
+        assert bool((buf[off:].view(43, 6, width)[..., 64:] == 5.0).all()) and bool((buf[:off] == 5.0).all())
+    one = q[:1].expand(6, 43, 64)                                 # one head's queries for all of them
+    got = mr.paged_attn(cache, table, lens, one, c.cu)
+    ref = mr.paged_attn(cache, table, lens, one.contiguous(), c.cu)
+    assert np.all(np.abs(np64(got) - np64(ref)) <= 2 * tol.max())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_attn_of_one_row_is_decode(mr, dt):
+    c = Case(mr, [1] * 4, [300, 1, 64, 129], 8, 2, 16, 128, dt, seed=9)
+    O, lse = mr.paged_attn(*c.args(), c.cu, window=100, sinks=5, return_lse=True, ws=c.ws)
+    P, lse2 = mr.paged_decode(*c.args(), window=100, sinks=5, return_lse=True, ws=c.ws)
+    c.check(O, lse, window=100, sinks=5, p_eps=ATTN_P[dt])
+    c.check(P, lse2, window=100, sinks=5, p_eps=DECODE_P[dt])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_attn_reports_bad_pages_and_short_tables(mr, dt):
+    c = Case(mr, [30, 20], [40, 20], 2, 1, 16, 64, dt, seed=10)
+    cache, table, lens, q = c.args()
+    want = mr.paged_attn(cache, table, lens, q, c.cu, ws=c.ws)
+    for bad in (-1, 10 ** 6):
+        t = table.clone()
+        t[0, 1] = bad
+        got = mr.paged_attn(cache, t, lens, q, c.cu, ws=c.ws)
+        assert c.ws.sync_status() == mr.MR_ERR_DEVICE_CHECK
+        assert torch.equal(got[:, 30:], want[:, 30:]) and bool(torch.isfinite(got).all())
+    t = table.clone()
+    t[0, 3:] = 10 ** 6
+    t[1, 2:] = -7
+    assert torch.equal(mr.paged_attn(cache, t, lens, q, c.cu, ws=c.ws), want) and c.ws.sync_status() == mr.MR_OK
+    mr.paged_attn(cache, table[:, :2].contiguous(), lens, q, c.cu, ws=c.ws)
+    assert c.ws.sync_status() == mr.MR_ERR_DEVICE_CHECK
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_attn_no_rows(mr, dt):
+    c = Case(mr, [0, 0], [40, 20], 2, 1, 16, 64, dt, seed=11, behind=2)
+    cache, table, lens, q = c.args()
+    out = torch.full_like(q, 5.0)
+    mr.paged_attn(cache, table, lens, q, c.cu, out=out, ws=c.ws)
+    assert bool((out == 5.0).all()) and c.ws.sync_status() == mr.MR_OK
+    assert mr.paged_attn(cache, table, lens, q[:, :0], c.cu).shape == (2, 0, 64)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_attn_on_a_stream_and_in_a_graph(mr, dt):
+    c = Case(mr, [50, 3, 200], [50, 80, 900], 8, 2, 16, 128, dt, seed=12)
+    cache, table, lens, q = c.args()
+    want, wl = mr.paged_attn(cache, table, lens, q, c.cu, return_lse=True, ws=c.ws)
+    out, lse = torch.zeros_like(want), torch.zeros_like(wl)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        mr.paged_attn(cache, table, lens, q, c.cu, out=out, lse=lse, ws=c.ws)
+    st.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mr.paged_attn(cache, table, lens, q, c.cu, out=out, lse=lse, ws=c.ws)
+    for n in (900, 500, 210):
+        lens[2] = n
+        out.zero_()
+        g.replay()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, mr.paged_attn(cache, table, lens, q, c.cu))

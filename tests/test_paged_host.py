@@ -142,6 +142,26 @@ def test_decode_refuses(mr):
     assert call(Hq=2048) == mr.MR_ERR_UNSUPPORTED
 
 
+def test_attn_refuses(mr):
+    x = mr.Rows(FAKE, 640, 64)
+    n_ws = mr.LIB.mr_paged_workspace_bytes(ctypes.byref(_cache(mr)), 4, 3)
+
+    def call(c=None, s=None, Q=x, Hq=4, cu=FAKE, total=10, scale=0.125, window=0, sinks=0, O=x, ws=FAKE, wsb=n_ws):
+        ref = lambda o: ctypes.byref(o) if o is not None else None
+        return mr.LIB.mr_paged_attn(ref(c or _cache(mr)), ref(s or _seqs(mr)), ref(Q), Hq, cu, total, scale, window, sinks,
+                                    ref(O), None, ws, wsb, None)
+    for kw, code in BAD_CACHES:
+        assert call(c=_cache(mr, **kw)) == code, kw
+    for kw in BAD_SEQS:
+        assert call(s=_seqs(mr, **kw)) == mr.MR_ERR_INVALID_ARG, kw
+    for kw in (dict(ws=None), dict(ws=FAKE + 8), dict(wsb=n_ws - 1), dict(Q=None), dict(O=None), dict(Hq=0), dict(Hq=5),
+               dict(scale=float("nan")), dict(scale=float("-inf")), dict(window=-1), dict(sinks=-1), dict(cu=None),
+               dict(total=-1), dict(Q=mr.Rows(FAKE, -640, 64)), dict(Q=mr.Rows(FAKE + 1, 640, 64)),
+               dict(O=mr.Rows(FAKE, 64, 64)), dict(O=mr.Rows(FAKE, 0, 64)), dict(O=mr.Rows(FAKE, 630, 64))):
+        assert call(**kw) == mr.MR_ERR_INVALID_ARG, kw
+    assert call(Hq=2048) == mr.MR_ERR_UNSUPPORTED
+
+
 def test_workspace_sizes(mr):
     n = lambda Hq=4, n_seq=3, **kw: mr.LIB.mr_paged_workspace_bytes(ctypes.byref(_cache(mr, **kw)), Hq, n_seq)
     assert n() >= 256 and n(d=96) == 0 and n(Hq=5) == 0 and n(Hq=0) == 0 and n(n_seq=0) == 0
