@@ -313,8 +313,10 @@ constexpr size_t kCounterBytes = (kAttnMaxCtas * sizeof(uint32_t) + 255) / 256 *
 
 }  // namespace
 
-size_t attn_workspace_bytes(int d) {
-  return kWsHeaderBytes + kCounterBytes + (size_t)2 * kAttnMaxCtas * kRows * (d + 2) * sizeof(float);
+size_t attn_workspace_bytes(mr_dtype dt, int d) {
+  const size_t simt = (size_t)2 * kAttnMaxCtas * kRows * (d + 2) * sizeof(float);
+  const size_t tc = dt == MR_BF16 ? attn_tc_part_bytes(d) : 0;
+  return kWsHeaderBytes + kCounterBytes + (simt > tc ? simt : tc);
 }
 
 void attn_split(AttnParams& p, int rows, int max_heads) {
@@ -353,6 +355,7 @@ cudaError_t launch_attn(const AttnArgs& a) {
   p.ws = (WsHeader*)a.ws;
   p.counters = (uint32_t*)((char*)a.ws + kWsHeaderBytes);
   p.part = (float*)((char*)a.ws + kWsHeaderBytes + kCounterBytes);
+  if (launch_attn_tc(a, p, sms, &e)) return e;
   attn_split(p, kRows, kMaxHeads);
   p.tokens = p.tile_tokens;
   p.min_steps = 2;

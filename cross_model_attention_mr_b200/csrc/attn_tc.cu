@@ -1,0 +1,821 @@
+// Attention of a chunk of new rows per sequence over the paged cache on the tensor cores (bf16; pages of a multiple of
+// 8 rows; rows of Q and O aligned to 16 bytes).
+//
+// A unit is two tiles A and B of 128 query rows: runs of new rows times the query heads that share a key head, so a key
+// tile serves the whole group, and one persistent CTA per SM walks its share of the units' key tiles (attn_units.cuh).
+// Tensor Memory holds S and O of both tiles; P takes the place of S.
+//   * producer warp: TMA loads of the query tiles (a box of rows x heads) and of key and value tiles page by page (a
+//     lane per box; what nobody sees is asked for outside the pool, which TMA fills with zeros), K_0, V_0, K_1, ...
+//     through a ring;
+//   * MMA thread: S_x(0) = Q_x K_0^T for both tiles, then for each key tile j and x in A, B: O_x += P_x(j) V_j with P
+//     from Tensor Memory, and S_x(j + 1) behind it, so one tile's products run during the other one's softmax.  S, P
+//     and O of a tile are ordered by the tensor core's own order, so no barrier says that P has been read;
+//   * two softmax warpgroups, a query row per thread: the mask only in tiles where some row does not see some key, a row
+//     reference that moves when a score passes it by 2^8 (O is then rescaled in Tensor Memory), P = 2^(x - reference)
+//     in bf16;
+//   * two fix-up warps look after the values of those tiles: rows that nobody of the unit sees become zeros (0 * NaN
+//     would not be 0); rows that only some see are searched for values that are not finite, and where there are any the
+//     segment's rows are computed again one by one.
+// Bound by the exponentials (16384 per tile at 16 a clock take as long as the tile's two products) and by the chain
+// S -> softmax -> P V -> S of each tile.
+// Every wait is bounded (MR_ERR_TIMEOUT, then drain and free Tensor Memory).
+#include <cuda_bf16.h>
+
+#include "attn_units.cuh"
+#include "kernels.h"
+#include "profile.h"
+#include "sm100.cuh"
+#include "tma_host.h"
+
+namespace mr {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 384;
+constexpr int kProducerWarp = 0;
+constexpr int kMmaWarp = 1;
+constexpr int kFixWarp0 = 2;
+constexpr int kSoftmaxWarp0 = 4;
+// Each SM sub-partition holds one warp of each warpgroup: 72 + 216 + 216 registers of the launch's 3 x 168.
+constexpr int kLaunchRegs = 168;
+constexpr int kRegsControl = 72;
+constexpr int kRegsSoftmax = 216;
+static_assert(kRegsControl + 2 * kRegsSoftmax == 3 * kLaunchRegs, "register split");
+constexpr int kKeys = 128;
+constexpr int kMaxHeads = 32;     // query heads of a tile at most
+constexpr int kMaxCtas = 152;     // one per SM
+constexpr int kSlowRing = 16;     // segments that can be under way at once, and more
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr float kRescale = 8.0f;
+constexpr int kPoly = 1;          // of 8 pairs of exponentials, those on the multiply-add pipe
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D>
+struct Smem {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kSlotBytes = kHalves * 128 * 128;
+  __nv_bfloat16 q[2][kHalves][128 * 64];         // [tile][column half][row][64]
+  __nv_bfloat16 kv[kSlots][kHalves][128 * 64];   // [slot][column half][key][64]
+  uint64_t q_full, q_empty;
+  uint64_t slot_full[kSlots], slot_empty[kSlots], slot_fixed[kSlots];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t part_done, join_go, mma_done;
+  PartitionSmem part;
+  uint32_t tmem_base;
+  int abort;
+  int slow[kSlowRing];  // segment number + 1 where the rows have to be computed one by one
+  int join;
+};
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+template <int D>
+__device__ __forceinline__ void fail(Smem<D>& s, const AttnParams& p, uint32_t detail) {
+  set_status(p.ws, MR_ERR_TIMEOUT, detail);
+  s.abort = 1;
+}
+
+// Rows of positions first .. last: is there a key of the tile at key0 that one of them does not see?
+__device__ __forceinline__ bool on_edge(const AttnParams& p, int first, int last, int held, int key0) {
+  return key0 + kKeys - 1 > min(first, held - 1) ||
+         (p.window > 0 && last >= p.window && key0 <= last - p.window && key0 + kKeys > p.sinks);
+}
+
+// Bits 0 .. n - 1, for any n.
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u; }
+
+// Key tiles of the segment that tile x of the unit needs (a front part of them), 0 for a missing tile.
+__device__ __forceinline__ int steps_of(const AttnParams& p, const Seg& sg, int x) {
+  if (x * p.tile_tokens >= sg.u.n) return 0;
+  const int hi = min(sg.u.pos0 + min((x + 1) * p.tile_tokens, sg.u.n) - 1, sg.u.held - 1);
+  return min(max(tiles_upto<kKeys>(sg.u, hi) - sg.j0, 0), sg.j1 - sg.j0);
+}
+
+// ------------------------------------------------------------------------------------------------
+template <int D>
+__device__ void producer(Smem<D>& s, const AttnParams& p, const Share& sh, const Maps& maps, int box_rows) {
+  constexpr int kSlots = Smem<D>::kSlots, kHalves = Smem<D>::kHalves;
+  const int lane = threadIdx.x & 31;
+  const int boxes = kKeys / box_rows;
+  const int nowhere = p.kv.n_pages * p.kv.H_kv * p.kv.page_rows;  // the row behind the pool
+  Segments<kKeys> walk(p, sh);
+  Seg sg;
+  uint32_t item = 0, segs = 0;
+  bool ok = true;
+  while (ok && walk.next(sg)) {
+    const Unit& u = sg.u;
+    if (segs > 0) ok = mbar_wait_sleep(&s.q_empty, (segs - 1) & 1, &s.abort, p.wait_ns, 64);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) {
+      if (lane == 0) fail(s, p, 0xA01);
+      break;
+    }
+    if (lane == 0) {
+      const int tiles = u.n > p.tile_tokens ? 2 : 1;
+      mbar_arrive_expect_tx(&s.q_full, (uint32_t)(tiles * kHalves * p.hp * p.tile_tokens * 128));
+      for (int x = 0; x < tiles; ++x)
+        for (int c = 0; c < kHalves; ++c)
+          tma_load_3d(&s.q[x][c][0], &maps.q, &s.q_full, 64 * c, u.q0 + x * p.tile_tokens, sg.h0);
+    }
+    ++segs;
+    const int hi = min(u.pos0 + u.n - 1, u.held - 1);
+    const int lo = p.window > 0 && u.pos0 >= p.window ? u.pos0 - p.window + 1 : 0;
+    auto lookup = [&](int j) {
+      const int key = tile_of(u, j) * kKeys + lane * box_rows;
+      if (j >= sg.j1 || lane >= boxes || key > hi || (key >= p.sinks && key + box_rows - 1 < lo)) return nowhere;
+      const int r = pool_row(p.kv, u.s, sg.g, key);
+      if (r < 0) set_status(p.ws, MR_ERR_DEVICE_CHECK, kBadPage);
+      return r < 0 ? nowhere : r;
+    };
+    int row = lookup(sg.j0);
+    for (int j = sg.j0; j < sg.j1 && ok; ++j) {
+      const int next_row = lookup(j + 1);
+      for (int kv = 0; kv < 2; ++kv, ++item) {
+        const int sl = item % kSlots;
+        const uint32_t use = item / kSlots;
+        if (use > 0) ok = mbar_wait_sleep(&s.slot_empty[sl], (use - 1) & 1, &s.abort, p.wait_ns, 64);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (lane == 0) fail(s, p, 0xA02);
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&s.slot_full[sl], Smem<D>::kSlotBytes);
+        __syncwarp();
+        if (lane < boxes)
+          for (int c = 0; c < kHalves; ++c)
+            tma_load_2d(&s.kv[sl][c][lane * box_rows * 64], kv ? &maps.v : &maps.k, &s.slot_full[sl], 64 * c, row);
+      }
+      row = next_row;
+    }
+  }
+  // no load may land after the CTA releases its shared memory
+  if (lane == 0) {
+    const int never = 0;
+    for (uint32_t i = item > (uint32_t)kSlots ? item - kSlots : 0; i < item; ++i)
+      mbar_wait(&s.slot_full[i % kSlots], (i / kSlots) & 1, &never, kTimeoutNs);
+    if (segs > 0) mbar_wait(&s.q_full, (segs - 1) & 1, &never, kTimeoutNs);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// The whole warp runs the loop, one elected lane issues: what the tensor core's instructions take (descriptors, Tensor
+// Memory addresses) then stays in uniform registers.  (One lane that ran it alone spent 1.0 us on a tile's 16 products,
+// which themselves take 0.54 us.)
+template <int D>
+__device__ void mma_issuer(Smem<D>& s, const AttnParams& p, const Share& sh) {
+  constexpr int kSlots = Smem<D>::kSlots;
+  constexpr uint32_t kSlotLo = Smem<D>::kSlotBytes >> 4;  // a slot further, in a descriptor's low word
+  constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
+  constexpr uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
+  const int lane = threadIdx.x & 31;
+  const uint32_t tbase = __shfl_sync(0xffffffffu, s.tmem_base, 0);
+  const bool leader = elect_one();
+  // Q and K: K-major (distance of 8-row groups 1024); V: MN-major (column halves 16 KB apart)
+  const uint64_t q_desc = sdesc_sw128(smem_u32(&s.q[0][0][0]), 16, 1024);
+  const uint64_t k_desc = sdesc_sw128(smem_u32(&s.kv[0][0][0]), 16, 1024);
+  const uint64_t v_desc = sdesc_sw128(smem_u32(&s.kv[0][0][0]), 128 * 128, 1024);
+  Segments<kKeys> walk(p, sh);
+  Seg sg;
+  uint32_t segs = 0, fixed = 0;    // fixed: a parity bit per slot
+  uint32_t slot = 0, round = 0;    // ring position of the segment's next item, and its use's parity
+  uint32_t pc[2] = {0, 0}, oc[2] = {0, 0};
+  uint32_t where = 0;
+  auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, &s.abort, p.wait_ns));
+    if (!ok) where = code;
+    return ok;
+  };
+  auto scores = [&](int x, uint32_t sl) {
+    const uint64_t qd = q_desc + x * kSlotLo, kd = k_desc + sl * kSlotLo;
+    if (leader) {
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * 128 * 128 + 32 * (kk & 3)) >> 4;
+        mma_bf16_ss(tbase + 256 * x, qd + off, kd + off, id_qk, kk > 0 ? 1u : 0u);
+      }
+      mma_commit(&s.s_full[x]);
+    }
+  };
+  bool ok = true;
+  while (ok && walk.next(sg)) {
+    const Unit& u = sg.u;
+    const int n = sg.j1 - sg.j0;
+    const int nx[2] = {steps_of(p, sg, 0), steps_of(p, sg, 1)};
+    ok = wait(&s.q_full, segs, 0xA11) && wait(&s.slot_full[slot], round, 0xA12);
+    if (!ok) break;
+    tc_fence_after();
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (nx[x] > 0) scores(x, slot);
+    if (leader) {
+      mma_commit(&s.slot_empty[slot]);
+      if (n == 1) mma_commit(&s.q_empty);
+    }
+    for (int j = 0; j < n && ok; ++j) {
+      if (++slot == kSlots) slot = 0, round ^= 1;
+      const uint32_t sv = slot, rv = round;
+      if (j + 1 < n && ++slot == kSlots) slot = 0, round ^= 1;
+      const uint32_t sk = slot, rk = round;
+      bool have_v = false, have_k = false;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (j >= nx[x] || !ok) continue;
+        if (!have_v) {
+          ok = wait(&s.slot_full[sv], rv, 0xA13);
+          if (ok && on_edge(p, u.pos0, u.pos0 + u.n - 1, u.held, tile_of(u, sg.j0 + j) * kKeys)) {
+            ok = wait(&s.slot_fixed[sv], fixed >> sv, 0xA14);
+            fixed ^= 1u << sv;
+          }
+          have_v = true;
+        }
+        if (ok && j == 0 && oc[x] > 0) ok = wait(&s.o_free[x], oc[x] - 1, 0xA15);
+        ok = ok && wait(&s.p_full[x], pc[x], 0xA16);
+        if (!ok) continue;
+        ++pc[x];
+        tc_fence_after();
+        const uint64_t vd = v_desc + sv * kSlotLo;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(tbase + 256 * x + 128, tbase + 256 * x + 8 * kk, vd + (2048 >> 4) * kk, id_pv,
+                        (j > 0 || kk > 0) ? 1u : 0u);
+        }
+        if (j == nx[x] - 1) {
+          if (leader) mma_commit(&s.o_full[x]);
+          ++oc[x];
+        } else {
+          if (!have_k) ok = wait(&s.slot_full[sk], rk, 0xA17);
+          have_k = true;
+          if (!ok) continue;
+          tc_fence_after();
+          scores(x, sk);
+        }
+      }
+      if (!ok) break;
+      if (leader) {
+        mma_commit(&s.slot_empty[sv]);
+        if (j + 1 < n) mma_commit(&s.slot_empty[sk]);
+        if (j + 2 == n) mma_commit(&s.q_empty);
+      }
+    }
+    if (++slot == kSlots) slot = 0, round ^= 1;
+    ++segs;
+  }
+  if (!ok && lane == 0) fail(s, p, where);
+  // every MMA of this warp completes before Tensor Memory is released
+  if (leader) mma_commit(&s.mma_done);
+  __syncwarp();
+  const int never = 0;
+  mbar_wait(&s.mma_done, 0, &never, kTimeoutNs);
+}
+
+// ------------------------------------------------------------------------------------------------
+// Two warps: warp w takes column half w (d = 64: every other 4 rows).  They follow the ring item by item, so that they
+// never mistake one use of a slot for another.
+template <int D>
+__device__ void fixer(Smem<D>& s, const AttnParams& p, const Share& sh, int w) {
+  constexpr int kSlots = Smem<D>::kSlots;
+  constexpr int kGroups = D == 128 ? 32 : 16;  // groups of 4 rows of a warp
+  const int lane = threadIdx.x & 31;
+  Segments<kKeys> walk(p, sh);
+  Seg sg;
+  uint32_t item = 0, segs = 0;
+  while (walk.next(sg)) {
+    const Unit& u = sg.u;
+    const int last = u.pos0 + u.n - 1;
+    const int hi = min(last, u.held - 1), all = min(u.pos0, u.held - 1);  // up to `all`: no row is too early
+    const int lo = p.window > 0 && u.pos0 >= p.window ? u.pos0 - p.window + 1 : 0;
+    const int from = p.window > 0 && last >= p.window ? last - p.window + 1 : 0;  // from here on: no window is past
+    for (int j = sg.j0; j < sg.j1; ++j) {
+      const int key0 = tile_of(u, j) * kKeys;
+      for (int kv = 0; kv < 2; ++kv, ++item) {
+        const int sl = item % kSlots;
+        bool ok = mbar_wait_sleep(&s.slot_full[sl], (item / kSlots) & 1, &s.abort, 2 * p.wait_ns, 64);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (lane == 0) fail(s, p, 0xA21);
+          return;
+        }
+        if (kv == 1 && on_edge(p, u.pos0, last, u.held, key0)) {
+          char* v = reinterpret_cast<char*>(&s.kv[sl][D == 128 ? w : 0][0]) + lane * 16 + (D == 128 ? 0 : w * 512);
+          constexpr int kStep = D == 128 ? 512 : 1024;
+          const int row0 = (lane >> 3) + (D == 128 ? 0 : 4 * w);
+          uint32_t bad = 0;
+#pragma unroll 1
+          for (int g0 = 0; g0 < kGroups; g0 += 8) {
+            uint4 y[8];
+            uint32_t dead = 0, look = 0;
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              const int key = key0 + row0 + (g0 + g) * (kStep / 128);
+              const uint32_t first = key < p.sinks;
+              const uint32_t d = (uint32_t)(key > hi) | ((uint32_t)(key < lo) & (first ^ 1u));
+              const uint32_t full = (uint32_t)(key <= all) & ((uint32_t)(key >= from) | first);
+              dead |= d << g;
+              look |= ((d | full) ^ 1u) << g;
+            }
+            if (__any_sync(0xffffffffu, look != 0)) {
+#pragma unroll
+              for (int g = 0; g < 8; ++g) y[g] = *reinterpret_cast<const uint4*>(v + (g0 + g) * kStep);
+#pragma unroll
+              for (int g = 0; g < 8; ++g) {
+                const uint32_t e[4] = {y[g].x, y[g].y, y[g].z, y[g].w};
+                uint32_t hit = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) hit |= (e[i] & 0x7f807f80u) + 0x00800080u;
+                // (an exponent of all ones carries into bit 15 or 31 when one is added to it)
+                bad |= (look >> g & 1u) ? hit & 0x80008000u : 0u;
+              }
+            }
+            if (__any_sync(0xffffffffu, dead != 0)) {
+#pragma unroll
+              for (int g = 0; g < 8; ++g)
+                if (dead >> g & 1u) *reinterpret_cast<uint4*>(v + (g0 + g) * kStep) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async_smem();
+          if (__any_sync(0xffffffffu, bad != 0) && lane == 0) *(volatile int*)&s.slow[segs % kSlowRing] = (int)segs + 1;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.slot_fixed[sl]);
+        }
+        if (lane == 0) mbar_arrive(&s.slot_empty[sl]);
+      }
+    }
+    ++segs;
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Where a part of a unit goes: 256 (reference, sum) pairs, then outputs as [column / 4][row] float4.
+template <int D>
+__device__ __forceinline__ float* slot_ptr(const AttnParams& p, int64_t slot) {
+  return p.part + slot * (256 * (D + 2));
+}
+
+template <int D>
+__device__ __forceinline__ float4* slot_out(float* slot, int c4, int row) {
+  return reinterpret_cast<float4*>(slot + 512) + c4 * 256 + row;
+}
+
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// The 32 rows of a warp one by one (a lane per D / 32 columns): where values that are not finite would reach rows that
+// do not see them.
+template <int D>
+__device__ __noinline__ void rows_one_by_one(const AttnParams& p, const Seg& sg, int x, int q4, bool whole, float* slot) {
+  constexpr int C = D / 32;
+  const int lane = threadIdx.x & 31;
+  const Unit& u = sg.u;
+  for (int i = 0; i < 32; ++i) {
+    const int r = 32 * q4 + i;
+    const int hh = (int)fast_div((uint32_t)r, p.by_tile_tokens);
+    const int tok = x * p.tile_tokens + r - hh * p.tile_tokens;
+    if (hh >= sg.heads || tok >= u.n) continue;
+    const int h = sg.h0 + hh, row = u.q0 + tok, pos = u.pos0 + tok;
+    const __nv_bfloat16* q = (const __nv_bfloat16*)p.q + (int64_t)h * p.q_head + (int64_t)row * p.q_row + C * lane;
+    float qf[C], acc[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      qf[c] = __bfloat162float(q[c]);
+      acc[c] = 0.f;
+    }
+    float m = -INFINITY, l = 0.f;
+    for (int j = sg.j0; j < sg.j1; ++j) {
+      const int key0 = tile_of(u, j) * kKeys;
+      for (int key = key0; key < key0 + kKeys; ++key) {
+        if (key > min(pos, u.held - 1) || (p.window > 0 && key <= pos - p.window && key >= p.sinks)) continue;
+        const int at = pool_row(p.kv, u.s, sg.g, key);
+        float kf[C], vf[C], sc = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const int64_t e = (int64_t)max(at, 0) * D + C * lane + c;
+          kf[c] = at < 0 ? 0.f : __bfloat162float(((const __nv_bfloat16*)p.kv.k)[e]);
+          vf[c] = at < 0 ? 0.f : __bfloat162float(((const __nv_bfloat16*)p.kv.v)[e]);
+          sc = fmaf(qf[c], kf[c], sc);
+        }
+#pragma unroll
+        for (int w = 16; w; w >>= 1) sc += __shfl_xor_sync(0xffffffffu, sc, w);
+        sc *= p.a;
+        float f = 1.f;
+        if (sc > m) {
+          f = ex2_approx(m - sc);
+          m = sc;
+        }
+        const float e = ex2_approx(sc - (m == -INFINITY ? 0.f : m));
+        l = fmaf(l, f, e);
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] = fmaf(acc[c], f, e * vf[c]);
+      }
+    }
+    if (whole) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      __nv_bfloat16* o = (__nv_bfloat16*)p.o + (int64_t)h * p.o_head + (int64_t)row * p.o_row + C * lane;
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] = __float2bfloat16_rn(acc[c] * inv);
+      if (lane == 0 && p.lse) p.lse[(int64_t)h * p.total_q + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    } else {
+      const int at = 128 * x + r;
+      if (lane == 0) __stcg(reinterpret_cast<float2*>(slot) + at, make_float2(m, l));
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int col = C * lane + c;
+        __stcg(reinterpret_cast<float*>(slot_out<D>(slot, col >> 2, at)) + (col & 3), acc[c]);
+      }
+    }
+  }
+}
+
+// The outputs of a warp's 32 rows from all parts of the unit; `own`: maximum and 1 / sum of this lane's row.  An item is 4 columns of a row; up to 8 parts of it
+// are under way at once.
+template <int D>
+__device__ __noinline__ void join_rows(const AttnParams& p, const Seg& sg, int x, int q4, int first, int lastc,
+                                       float2 own) {
+  const int lane = threadIdx.x & 31;
+  // rows of the warp that exist, as a mask: head r / tile_tokens, new row r % tile_tokens
+  const int r0 = 32 * q4 + lane;
+  const int hh0 = (int)fast_div((uint32_t)r0, p.by_tile_tokens);
+  const bool mine = hh0 < sg.heads && x * p.tile_tokens + r0 - hh0 * p.tile_tokens < sg.u.n;
+  const uint32_t mask = __ballot_sync(0xffffffffu, mine);
+  const int n = __popc(mask);
+  const int kth = (int)__fns(mask, 0, lane + 1);  // the lane-th row that exists
+  for (int e0 = 0; e0 < n * (D / 4); e0 += 32) {
+    const int e = e0 + lane;
+    const int c4 = e / n;
+    const int i = __shfl_sync(0xffffffffu, kth, e - c4 * n);
+    const float2 mi = make_float2(__shfl_sync(0xffffffffu, own.x, i), __shfl_sync(0xffffffffu, own.y, i));
+    if (c4 >= D / 4) continue;
+    const int r = 32 * q4 + i, at = 128 * x + r;
+    const int hh = (int)fast_div((uint32_t)r, p.by_tile_tokens);
+    const int tok = x * p.tile_tokens + r - hh * p.tile_tokens;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = first; c0 <= lastc; c0 += 8) {
+      float4 y[8];
+      float2 ml[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        ml[b] = make_float2(-INFINITY, 0.f);
+        y[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c0 + b <= lastc) {
+          float* part = slot_ptr<D>(p, slot_of(c0 + b, first));
+          ml[b] = __ldcg(reinterpret_cast<const float2*>(part) + at);
+          y[b] = __ldcg(slot_out<D>(part, c4, at));
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        const float w = ex2_approx(ml[b].x - mi.x) * mi.y;
+        // (a part without a key of this row left its outputs unwritten)
+        const bool none = ml[b].x == -INFINITY && ml[b].y == 0.f;
+        acc.x = none ? acc.x : fmaf(w, y[b].x, acc.x);
+        acc.y = none ? acc.y : fmaf(w, y[b].y, acc.y);
+        acc.z = none ? acc.z : fmaf(w, y[b].z, acc.z);
+        acc.w = none ? acc.w : fmaf(w, y[b].w, acc.w);
+      }
+    }
+    __nv_bfloat16* o = (__nv_bfloat16*)p.o + (int64_t)(sg.h0 + hh) * p.o_head + (int64_t)(sg.u.q0 + tok) * p.o_row + 4 * c4;
+    *reinterpret_cast<uint2*>(o) = make_uint2(pack2(acc.x, acc.y), pack2(acc.z, acc.w));
+  }
+}
+
+// P = 2^(a v + neg) as bf16 pairs into Tensor Memory, and the sum.  Of every 8 pairs, the first Poly take the polynomial
+// on the multiply-add pipe instead of the multi-function unit (which gives exactly 0 for a masked -infinity).
+template <int Poly>
+__device__ __forceinline__ void exponentials(const float (&v)[128], float a, float neg, uint32_t addr, float2 (&sum)[2]) {
+  const float2 a2 = make_float2(a, a), n2 = make_float2(neg, neg);
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    uint32_t pk[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float2 x = fma2(make_float2(v[64 * b + 2 * e], v[64 * b + 2 * e + 1]), a2, n2);
+      const float2 y = (e & 7) < Poly ? ex2_poly2(x) : make_float2(ex2_approx(x.x), ex2_approx(x.y));
+      sum[e & 1] = add2(sum[e & 1], y);
+      pk[e] = pack2(y.x, y.y);
+    }
+    tmem_st32(addr + 32 * b, pk);
+  }
+}
+
+// Softmax warpgroup of tile x: S_x and P_x at Tensor Memory column 256 x, O_x at 256 x + 128.
+template <int D>
+__device__ void softmax_group(Smem<D>& s, const AttnParams& p, const Share& sh, int x) {
+  const uint64_t wait_ns = 2 * p.wait_ns;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q4 = warp & 3;
+  const int r = 32 * q4 + lane;  // row of the query tile
+  const uint32_t lane_addr = (uint32_t)(32 * q4) << 16;
+  const uint32_t s_addr = s.tmem_base + lane_addr + 256 * x, o_addr = s_addr + 128;
+  const int hh = (int)fast_div((uint32_t)r, p.by_tile_tokens);
+  const int tok = x * p.tile_tokens + r - hh * p.tile_tokens;
+  Segments<kKeys> walk(p, sh);
+  Seg sg;
+  uint32_t sc = 0, oc = 0, segs = 0, joins = 0;
+  for (; walk.next(sg); ++segs) {
+    const Unit& u = sg.u;
+    const bool whole = sg.whole();
+    if (whole && x * p.tile_tokens >= u.n) continue;
+    const bool row_ok = hh < sg.heads && tok < u.n;
+    const int pos = u.pos0 + tok;
+    const int last = row_ok ? min(pos, u.held - 1) : -1;  // last row seen
+    const int first_pos = u.pos0 + x * p.tile_tokens;
+    const int last_pos = u.pos0 + min((x + 1) * p.tile_tokens, u.n) - 1;
+    const int nx = steps_of(p, sg, x);
+    float ref = -INFINITY;  // row reference (base 2)
+    float l = 0.f;          // row sum of 2^(x - ref)
+    for (int j = 0; j < nx; ++j, ++sc) {
+      if (!mbar_wait(&s.s_full[x], sc & 1, &s.abort, wait_ns)) {
+        fail(s, p, 0xA31);
+        return;
+      }
+      __syncwarp();
+      tc_fence_after();
+      uint32_t raw[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, raw[c]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32_done(raw[c]);
+      float v[128];
+#pragma unroll
+      for (int e = 0; e < 128; ++e) v[e] = __uint_as_float(raw[e >> 5][e & 31]);
+      if (p.negate) {
+#pragma unroll
+        for (int e = 0; e < 128; ++e) v[e] = -v[e];
+      }
+      const int key0 = tile_of(u, sg.j0 + j) * kKeys;
+      const bool edge = on_edge(p, first_pos, last_pos, u.held, key0);
+      if (edge) {
+        const int hi = last - key0;                                                      // seen: up to hi ...
+        const int lo = p.window > 0 && pos >= p.window ? pos - p.window + 1 - key0 : 0;  // ... from lo on, or
+        const int sk = p.sinks - key0;                                                   // below sk
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t seen = (below(hi + 1 - 32 * c) & ~below(lo - 32 * c)) | (below(sk - 32 * c) & below(hi + 1 - 32 * c));
+#pragma unroll
+          for (int t = 0; t < 32; ++t) v[32 * c + t] = (seen & (1u << t)) ? v[32 * c + t] : -INFINITY;
+        }
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < 128; e += 8)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx[c] = max3_nan(mx[c], v[e + 2 * c], v[e + 2 * c + 1]);
+      const float mt = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * p.a;
+      // The reference (base 2) moves to the row maximum at the first finite score and whenever a score passes it by
+      // more than 2^8.  (S_x(j) is complete, so P_x(j - 1) V_{j-1} in front of it is too, and O_x may be changed.)
+      const bool need = ref == -INFINITY ? mt > -INFINITY : mt - ref > kRescale;
+      if (__any_sync(0xffffffffu, need)) {
+        const float f = !need ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx(ref - mt));
+        if (j > 0) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + 32 * c, o);
+            tmem_wait_ld();
+            tmem_ld32_done(o);
+#pragma unroll
+            for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * f);
+            tmem_st32(o_addr + 32 * c, o);
+          }
+          tmem_wait_st();
+        }
+        if (need) ref = mt;
+        l *= f;
+      }
+      // (a score of NaN or +infinity makes the row NaN: the polynomial would not)
+      const float neg = !(mt < INFINITY) ? __int_as_float(0x7fffffff) : (ref == -INFINITY ? 0.f : -ref);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      if (edge)
+        exponentials<0>(v, p.a, neg, s_addr, sum);
+      else
+        exponentials<kPoly>(v, p.a, neg, s_addr, sum);
+      sum[0] = add2(sum[0], sum[1]);
+      l += sum[0].x + sum[0].y;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.p_full[x]);
+    }
+    if (nx > 0) {
+      if (!mbar_wait(&s.o_full[x], oc & 1, &s.abort, wait_ns)) {
+        fail(s, p, 0xA32);
+        return;
+      }
+      ++oc;
+      __syncwarp();
+      tc_fence_after();
+    }
+    const bool slow = nx > 0 && *(volatile int*)&s.slow[segs % kSlowRing] == (int)segs + 1;
+    const int row = u.q0 + tok, h = sg.h0 + hh;
+    __nv_bfloat16* orow = (__nv_bfloat16*)p.o + (int64_t)h * p.o_head + (int64_t)row * p.o_row;
+    const int at = 128 * x + r;
+    int first = 0, lastc = 0;
+    float* slot = nullptr;
+    if (!whole) {
+      holders(sh, sg, first, lastc);
+      slot = slot_ptr<D>(p, slot_of(blockIdx.x, first));
+    }
+    if (slow) {
+      rows_one_by_one<D>(p, sg, x, q4, whole, slot);
+    } else {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (whole) {
+        if (row_ok && p.lse) p.lse[(int64_t)h * p.total_q + row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+      } else {
+        __stcg(reinterpret_cast<float2*>(slot) + at, make_float2(ref, l));
+      }
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        __syncwarp();
+        if (nx > 0) {
+          tmem_ld32(o_addr + 32 * c, o);
+          tmem_wait_ld();
+          tmem_ld32_done(o);
+        } else {
+#pragma unroll
+          for (int t = 0; t < 32; ++t) o[t] = 0;
+        }
+        if (!row_ok) continue;
+        if (whole) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint32_t q[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              q[e] = pack2(__uint_as_float(o[8 * g + 2 * e]) * inv, __uint_as_float(o[8 * g + 2 * e + 1]) * inv);
+            *reinterpret_cast<uint4*>(orow + 32 * c + 8 * g) = make_uint4(q[0], q[1], q[2], q[3]);
+          }
+        } else {
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            __stcg(slot_out<D>(slot, 8 * c + g, at),
+                   make_float4(__uint_as_float(o[4 * g]), __uint_as_float(o[4 * g + 1]), __uint_as_float(o[4 * g + 2]),
+                               __uint_as_float(o[4 * g + 3])));
+        }
+      }
+    }
+    tc_fence_before();
+    if (!whole) __threadfence();
+    __syncwarp();
+    if (lane == 0 && nx > 0) mbar_arrive(&s.o_free[x]);
+    if (whole) continue;
+    // the CTA that comes last joins the unit's parts
+    if (lane == 0) mbar_arrive(&s.part_done);
+    if (warp == kSoftmaxWarp0 && lane == 0) {
+      if (!mbar_wait(&s.part_done, joins & 1, &s.abort, wait_ns)) {
+        fail(s, p, 0xA33);
+      } else {
+        __threadfence();
+        s.join = atomicAdd(p.counters + first, 1u) == (uint32_t)(lastc - first);
+        mbar_arrive(&s.join_go);
+      }
+    }
+    __syncwarp();
+    if (!mbar_wait(&s.join_go, joins & 1, &s.abort, wait_ns)) {
+      fail(s, p, 0xA34);
+      return;
+    }
+    const bool join = *(volatile int*)&s.join != 0;
+    ++joins;
+    if (!join) continue;
+    __threadfence();
+    // this thread's row: the maximum and the sum over all parts
+    float2 own = make_float2(0.f, 0.f);
+    if (row_ok) {
+      float m = -INFINITY, sum = 0.f;
+      for (int c0 = first; c0 <= lastc; c0 += 8) {
+        float2 ml[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          ml[i] = c0 + i <= lastc ? __ldcg(reinterpret_cast<const float2*>(slot_ptr<D>(p, slot_of(c0 + i, first))) + at)
+                                  : make_float2(-INFINITY, 0.f);
+        float mm = m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mm = fmaxf(mm, ml[i].x);
+        const float m0 = mm == -INFINITY ? 0.f : mm;
+        sum *= ex2_approx(m - m0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(ex2_approx(ml[i].x - m0), ml[i].y, sum);
+        m = mm;
+      }
+      own = make_float2(m == -INFINITY ? 0.f : m, sum == 0.f ? 0.f : 1.f / sum);
+      if (p.lse) p.lse[(int64_t)h * p.total_q + row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+    }
+    __syncwarp();
+    join_rows<D>(p, sg, x, q4, first, lastc, own);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnParams p, int box_rows) {
+  extern __shared__ unsigned char smem_raw[];
+  Smem<D>& s = *reinterpret_cast<Smem<D>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  empty_rows<__nv_bfloat16, D, kThreads>(p);
+  Share sh;
+  if (!make_share<kKeys, kThreads>(p, s.part, sh)) return;  // nothing for this CTA (all its threads leave)
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    mbar_init(&s.q_full, 1);
+    mbar_init(&s.q_empty, 1);
+    for (int i = 0; i < Smem<D>::kSlots; ++i) {
+      mbar_init(&s.slot_full[i], 1);
+      mbar_init(&s.slot_empty[i], 3);  // the MMAs that read it, and the fix-up warps
+      mbar_init(&s.slot_fixed[i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.p_full[i], 4);
+      mbar_init(&s.o_full[i], 1);
+      mbar_init(&s.o_free[i], 4);
+    }
+    mbar_init(&s.part_done, 8);
+    mbar_init(&s.join_go, 1);
+    mbar_init(&s.mma_done, 1);
+    s.abort = 0;
+    for (int i = 0; i < kSlowRing; ++i) s.slow[i] = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&s.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp < kSoftmaxWarp0) {
+    regs_dec<kRegsControl>();
+    if (warp == kProducerWarp)
+      producer<D>(s, p, sh, maps, box_rows);
+    else if (warp == kMmaWarp)
+      mma_issuer<D>(s, p, sh);
+    else
+      fixer<D>(s, p, sh, warp - kFixWarp0);
+  } else {
+    regs_inc<kRegsSoftmax>();
+    softmax_group<D>(s, p, sh, (warp - kSoftmaxWarp0) >> 2);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(s.tmem_base, 512);
+}
+
+template <int D>
+cudaError_t launch(const Maps& maps, const AttnParams& p, int box_rows, int grid, cudaStream_t st) {
+  // the register split assumes the launch allocation it was sized for; anything else could leave an increase waiting
+  // for registers that do not exist
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, k_attn_tc<D>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  const size_t smem = sizeof(Smem<D>) + 1024;
+  e = cudaFuncSetAttribute(k_attn_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  ProfScope ps(kKAttnTc, st);
+  k_attn_tc<D><<<grid, kThreads, smem, st>>>(maps, p, box_rows);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attn_tc_part_bytes(int d) { return (size_t)2 * kMaxCtas * 256 * (d + 2) * sizeof(float); }
+
+bool launch_attn_tc(const AttnArgs& a, AttnParams p, int sms, cudaError_t* result) {
+  if (a.dt != MR_BF16 || a.kv.page_rows % 8 || !p.vec_q || !p.vec_o) return false;
+  attn_split(p, 128, kMaxHeads);
+  p.tokens = 2 * p.tile_tokens;
+  p.min_steps = 2;
+  int box = 8;  // rows of a page that one copy takes
+  while (box < kKeys && a.kv.page_rows % (2 * box) == 0) box *= 2;
+  const int d = a.kv.d;
+  const uint64_t rows = (uint64_t)a.kv.n_pages * a.kv.H_kv * a.kv.page_rows;
+  Maps maps;
+  // a stride that is never taken may be anything
+  const uint64_t q_row = a.total_q > 1 ? (uint64_t)a.q.row_stride * 2 : (uint64_t)d * 2;
+  const uint64_t q_head = a.H_q > 1 ? (uint64_t)a.q.head_stride * 2 : (uint64_t)d * 2;
+  if (q_row == 0 || q_head == 0) return false;
+  if (!make_tmap_bf16_3d(&maps.q, a.q.ptr, d, a.total_q, a.H_q, q_row, q_head, 64, p.tile_tokens, p.hp) ||
+      !make_tmap_bf16_2d(&maps.k, a.kv.k, d, rows, (uint64_t)d * 2, 64, box) ||
+      !make_tmap_bf16_2d(&maps.v, a.kv.v, d, rows, (uint64_t)d * 2, 64, box))
+    return false;
+  // the running maximum is taken of the products before they are scaled, so the scale is kept positive (0 becomes so
+  // small that no score counts; masked ones stay -infinity)
+  p.negate = p.a < 0.f;
+  p.a = p.a == 0.f ? 1e-30f : fabsf(p.a);
+  p.wait_ns = kTimeoutNs;
+  const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+  *result = d == 64 ? launch<64>(maps, p, box, grid, a.stream) : launch<128>(maps, p, box, grid, a.stream);
+  return true;
+}
+
+}  // namespace mr

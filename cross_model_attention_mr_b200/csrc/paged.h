@@ -81,7 +81,10 @@ struct AttnArgs {
 struct AttnParams;
 constexpr int kAttnMaxCtas = 304;  // two per SM (148) at most; sizes counters and partial results
 
-size_t attn_workspace_bytes(int d);
+size_t attn_workspace_bytes(mr_dtype dt, int d);
+size_t attn_tc_part_bytes(int d);  // partial results of the tensor-core kernel
+// The tensor-core kernel, where it takes the call (false: it does not).
+bool launch_attn_tc(const AttnArgs& a, AttnParams p, int sms, cudaError_t* result);
 // chunks of at most max_heads query heads, and the new rows that a tile of `rows` query rows takes of each
 void attn_split(AttnParams& p, int rows, int max_heads);
 cudaError_t launch_attn(const AttnArgs& a);

@@ -101,7 +101,7 @@ mr_status mr_rope_apply(const mr_rope* rope, const mr_rows* X, const mr_rows* Y,
 
 size_t mr_paged_workspace_bytes(const mr_kv_cache* cache, int H_q, int n_seq) {
   if (cache_ok(cache) != MR_OK || H_q < 1 || H_q > kMaxHeads || H_q % cache->H_kv || n_seq < 1) return 0;
-  const size_t dec = decode_workspace_bytes(cache->d), att = attn_workspace_bytes(cache->d);
+  const size_t dec = decode_workspace_bytes(cache->d), att = attn_workspace_bytes(cache->dt, cache->d);
   return dec > att ? dec : att;
 }
 

@@ -38,4 +38,23 @@ bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t planes,
+                       uint64_t row_bytes, uint64_t plane_bytes, uint32_t box_cols, uint32_t box_rows,
+                       uint32_t box_planes) {
+  std::call_once(g_once, resolve);
+  if (!g_encode) return false;
+  if ((reinterpret_cast<uintptr_t>(base) & 15u) != 0 || ((row_bytes | plane_bytes) & 15u) != 0) return false;
+  if ((row_bytes | plane_bytes) >> 40) return false;
+  if (box_cols * 2u > 128u || box_rows > 256u || box_planes > 256u) return false;
+  cuuint64_t dims[3] = {cols, rows, planes};
+  cuuint64_t strides[2] = {row_bytes, plane_bytes};
+  cuuint32_t box[3] = {box_cols, box_rows, box_planes};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace mr
