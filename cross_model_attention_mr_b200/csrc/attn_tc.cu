@@ -7,15 +7,14 @@
 //   * producer warp: TMA loads of the query tiles (a box of rows x heads) and of key and value tiles page by page (a
 //     lane per box; what nobody sees is asked for outside the pool, which TMA fills with zeros), K_0, V_0, K_1, ...
 //     through a ring;
-//   * MMA thread: S_x(0) = Q_x K_0^T for both tiles, then for each key tile j and x in A, B: O_x += P_x(j) V_j with P
-//     from Tensor Memory, and S_x(j + 1) behind it, so one tile's products run during the other one's softmax.  S, P
-//     and O of a tile are ordered by the tensor core's own order, so no barrier says that P has been read;
-//   * two softmax warpgroups, a query row per thread: the mask only in tiles where some row does not see some key, a row
-//     reference that moves when a score passes it by 2^8 (O is then rescaled in Tensor Memory), P = 2^(x - reference)
-//     in bf16;
-//   * two fix-up warps look after the values of those tiles: rows that nobody of the unit sees become zeros (0 * NaN
-//     would not be 0); rows that only some see are searched for values that are not finite, and where there are any the
-//     segment's rows are computed again one by one.
+//   * an MMA warp for each tile: S(0) = Q K_0^T, then for each key tile j O += P(j) V_j, in two halves as P is handed
+//     over, and S(j + 1) behind it, so one tile's products run during the other one's softmax.  S, P and O of a tile are
+//     ordered by the tensor core's own order, so no barrier says that P has been read;
+//   * two softmax warpgroups, a query row per thread: the mask only where some row does not see some key, a row reference
+//     that moves when a score passes it by 2^8 (O is then rescaled in Tensor Memory), P = 2^(x - reference) in bf16;
+//   * a fix-up warp looks after the values of key tiles that not every row sees: rows that nobody of the unit sees become
+//     zeros (0 * NaN would not be 0); rows that only some see are searched for values that are not finite, and where
+//     there are any the segment's rows are computed again one by one.
 // Bound by the exponentials (16384 per tile at 16 a clock take as long as the tile's two products) and by the chain
 // S -> softmax -> P V -> S of each tile.
 // Every wait is bounded (MR_ERR_TIMEOUT, then drain and free Tensor Memory).
@@ -34,21 +33,23 @@ using namespace sm100;
 
 constexpr int kThreads = 384;
 constexpr int kProducerWarp = 0;
-constexpr int kMmaWarp = 1;
-constexpr int kFixWarp0 = 2;
+constexpr int kMmaWarp0 = 1;      // tile A; tile B: warp 3
+constexpr int kFixWarp = 2;
 constexpr int kSoftmaxWarp0 = 4;
+constexpr int kSoftmaxWarps = 8;  // a warpgroup for each tile
 // Each SM sub-partition holds one warp of each warpgroup: 72 + 216 + 216 registers of the launch's 3 x 168.
 constexpr int kLaunchRegs = 168;
 constexpr int kRegsControl = 72;
 constexpr int kRegsSoftmax = 216;
 static_assert(kRegsControl + 2 * kRegsSoftmax == 3 * kLaunchRegs, "register split");
 constexpr int kKeys = 128;
+constexpr int kHalf = 64;         // keys whose P is handed over at a time
 constexpr int kMaxHeads = 32;     // query heads of a tile at most
 constexpr int kMaxCtas = 152;     // one per SM
 constexpr int kSlowRing = 16;     // segments that can be under way at once, and more
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr float kRescale = 8.0f;
-constexpr int kPoly = 1;          // of 8 pairs of exponentials, those on the multiply-add pipe
+constexpr int kLate = 40;         // pairs of exponentials before the first half of P is handed over
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
@@ -60,7 +61,8 @@ struct Smem {
   __nv_bfloat16 kv[kSlots][kHalves][128 * 64];   // [slot][column half][key][64]
   uint64_t q_full, q_empty;
   uint64_t slot_full[kSlots], slot_empty[kSlots], slot_fixed[kSlots];
-  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t s_full[2], p_full[2][2];              // [tile], [tile][key half]
+  uint64_t o_full[2], o_free[2];
   uint64_t part_done, join_go, mma_done;
   PartitionSmem part;
   uint32_t tmem_base;
@@ -79,10 +81,16 @@ __device__ __forceinline__ void fail(Smem<D>& s, const AttnParams& p, uint32_t d
   s.abort = 1;
 }
 
-// Rows of positions first .. last: is there a key of the tile at key0 that one of them does not see?
-__device__ __forceinline__ bool on_edge(const AttnParams& p, int first, int last, int held, int key0) {
-  return key0 + kKeys - 1 > min(first, held - 1) ||
-         (p.window > 0 && last >= p.window && key0 <= last - p.window && key0 + kKeys > p.sinks);
+// mbar_wait by a whole warp for the phase with `n`'s parity: all lanes go on, or none.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t n, const volatile int* abort, uint64_t ns) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, n & 1, abort, ns));
+}
+
+// Rows of positions first .. last: is there one of the N keys from key0 on that some row does not see?
+template <int N>
+__device__ __forceinline__ bool on_edge(int window, int sinks, int first, int last, int held, int key0) {
+  return (key0 + N - 1 > min(first, held - 1)) |
+         ((window > 0) & (last >= window) & (key0 <= last - window) & (key0 + N > sinks));
 }
 
 // Bits 0 .. n - 1, for any n.
@@ -162,108 +170,94 @@ __device__ void producer(Smem<D>& s, const AttnParams& p, const Share& sh, const
 }
 
 // ------------------------------------------------------------------------------------------------
-// The whole warp runs the loop, one elected lane issues: what the tensor core's instructions take (descriptors, Tensor
-// Memory addresses) then stays in uniform registers.  (One lane that ran it alone spent 1.0 us on a tile's 16 products,
-// which themselves take 0.54 us.)
+// A warp per tile.  The whole warp runs the loop, one elected lane issues: what the tensor core's instructions take
+// (descriptors, Tensor Memory addresses) then stays in uniform registers.  (One lane that ran it alone spent 1.0 us on a
+// tile's 16 products, which themselves take 0.54 us.)  Items of the ring that this tile does not need are passed on.
 template <int D>
-__device__ void mma_issuer(Smem<D>& s, const AttnParams& p, const Share& sh) {
+__device__ void mma_issuer(Smem<D>& s, const AttnParams& p, const Share& sh, int x) {
   constexpr int kSlots = Smem<D>::kSlots;
   constexpr uint32_t kSlotLo = Smem<D>::kSlotBytes >> 4;  // a slot further, in a descriptor's low word
-  constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
+  const uint32_t id_qk = idesc_bf16_f32(128, kKeys, false, false) | (p.negate ? kIdescNegateA : 0u);
   constexpr uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
   const int lane = threadIdx.x & 31;
-  const uint32_t tbase = __shfl_sync(0xffffffffu, s.tmem_base, 0);
+  const uint32_t s_col = __shfl_sync(0xffffffffu, s.tmem_base, 0) + 256 * x, o_col = s_col + 128;
   const bool leader = elect_one();
   // Q and K: K-major (distance of 8-row groups 1024); V: MN-major (column halves 16 KB apart)
-  const uint64_t q_desc = sdesc_sw128(smem_u32(&s.q[0][0][0]), 16, 1024);
+  const uint64_t q_desc = sdesc_sw128(smem_u32(&s.q[x][0][0]), 16, 1024);
   const uint64_t k_desc = sdesc_sw128(smem_u32(&s.kv[0][0][0]), 16, 1024);
   const uint64_t v_desc = sdesc_sw128(smem_u32(&s.kv[0][0][0]), 128 * 128, 1024);
   Segments<kKeys> walk(p, sh);
   Seg sg;
-  uint32_t segs = 0, fixed = 0;    // fixed: a parity bit per slot
-  uint32_t slot = 0, round = 0;    // ring position of the segment's next item, and its use's parity
-  uint32_t pc[2] = {0, 0}, oc[2] = {0, 0};
-  uint32_t where = 0;
+  uint32_t segs = 0, fixed = 0;        // fixed: a parity bit per slot
+  uint32_t slot = 0, round = 0;        // ring position of the next item, and its use's parity
+  uint32_t pc = 0, oc = 0, where = 0;  // P tiles and outputs so far
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, &s.abort, p.wait_ns));
+    const bool ok = warp_wait(bar, parity, &s.abort, p.wait_ns);
     if (!ok) where = code;
     return ok;
   };
-  auto scores = [&](int x, uint32_t sl) {
-    const uint64_t qd = q_desc + x * kSlotLo, kd = k_desc + sl * kSlotLo;
-    if (leader) {
+  // S = Q K^T of the item at hand (or nothing), which is then passed on
+  auto key_item = [&](bool use, bool last) {
+    if (!wait(&s.slot_full[slot], round, 0xA12)) return false;
+    if (use) {
+      tc_fence_after();
+      const uint64_t kd = k_desc + slot * kSlotLo;
+      if (leader) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = ((kk >> 2) * 128 * 128 + 32 * (kk & 3)) >> 4;
-        mma_bf16_ss(tbase + 256 * x, qd + off, kd + off, id_qk, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * 128 * 128 + 32 * (kk & 3)) >> 4;
+          mma_bf16_ss(s_col, q_desc + off, kd + off, id_qk, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&s.s_full[x]);
+        mma_commit(&s.slot_empty[slot]);
+        if (last) mma_commit(&s.q_empty);
       }
-      mma_commit(&s.s_full[x]);
+    } else if (lane == 0) {
+      mbar_arrive(&s.slot_empty[slot]);
     }
+    if (++slot == kSlots) slot = 0, round ^= 1;
+    return true;
   };
   bool ok = true;
   while (ok && walk.next(sg)) {
     const Unit& u = sg.u;
-    const int n = sg.j1 - sg.j0;
-    const int nx[2] = {steps_of(p, sg, 0), steps_of(p, sg, 1)};
-    ok = wait(&s.q_full, segs, 0xA11) && wait(&s.slot_full[slot], round, 0xA12);
-    if (!ok) break;
-    tc_fence_after();
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-      if (nx[x] > 0) scores(x, slot);
-    if (leader) {
-      mma_commit(&s.slot_empty[slot]);
-      if (n == 1) mma_commit(&s.q_empty);
-    }
+    const int n = sg.j1 - sg.j0, nx = steps_of(p, sg, x);
+    ok = wait(&s.q_full, segs++, 0xA11);
+    if (ok && nx == 0 && lane == 0) mbar_arrive(&s.q_empty);
+    ok = ok && key_item(nx > 0, nx == 1);
     for (int j = 0; j < n && ok; ++j) {
-      if (++slot == kSlots) slot = 0, round ^= 1;
-      const uint32_t sv = slot, rv = round;
-      if (j + 1 < n && ++slot == kSlots) slot = 0, round ^= 1;
-      const uint32_t sk = slot, rk = round;
-      bool have_v = false, have_k = false;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (j >= nx[x] || !ok) continue;
-        if (!have_v) {
-          ok = wait(&s.slot_full[sv], rv, 0xA13);
-          if (ok && on_edge(p, u.pos0, u.pos0 + u.n - 1, u.held, tile_of(u, sg.j0 + j) * kKeys)) {
-            ok = wait(&s.slot_fixed[sv], fixed >> sv, 0xA14);
-            fixed ^= 1u << sv;
-          }
-          have_v = true;
-        }
-        if (ok && j == 0 && oc[x] > 0) ok = wait(&s.o_free[x], oc[x] - 1, 0xA15);
-        ok = ok && wait(&s.p_full[x], pc[x], 0xA16);
-        if (!ok) continue;
-        ++pc[x];
-        tc_fence_after();
-        const uint64_t vd = v_desc + sv * kSlotLo;
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tbase + 256 * x + 128, tbase + 256 * x + 8 * kk, vd + (2048 >> 4) * kk, id_pv,
-                        (j > 0 || kk > 0) ? 1u : 0u);
-        }
-        if (j == nx[x] - 1) {
-          if (leader) mma_commit(&s.o_full[x]);
-          ++oc[x];
-        } else {
-          if (!have_k) ok = wait(&s.slot_full[sk], rk, 0xA17);
-          have_k = true;
-          if (!ok) continue;
-          tc_fence_after();
-          scores(x, sk);
-        }
+      ok = wait(&s.slot_full[slot], round, 0xA13);
+      if (ok && on_edge<kKeys>(p.window, p.sinks, u.pos0, u.pos0 + u.n - 1, u.held, tile_of(u, sg.j0 + j) * kKeys)) {
+        if (j < nx) ok = wait(&s.slot_fixed[slot], fixed >> slot, 0xA14);
+        fixed ^= 1u << slot;
       }
+      if (ok && j == 0 && nx > 0 && oc > 0) ok = wait(&s.o_free[x], oc - 1, 0xA15);
       if (!ok) break;
-      if (leader) {
-        mma_commit(&s.slot_empty[sv]);
-        if (j + 1 < n) mma_commit(&s.slot_empty[sk]);
-        if (j + 2 == n) mma_commit(&s.q_empty);
+      if (j < nx) {
+        const uint64_t vd = v_desc + slot * kSlotLo;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (ok) ok = wait(&s.p_full[x][h], pc, 0xA16);
+          tc_fence_after();
+          if (leader && ok) {
+#pragma unroll
+            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+              mma_bf16_ts(o_col, s_col + 8 * kk, vd + (2048 >> 4) * kk, id_pv, (j > 0 || kk > 0) ? 1u : 0u);
+          }
+        }
+        if (!ok) break;
+        ++pc;
+        if (leader) {
+          mma_commit(&s.slot_empty[slot]);
+          if (j == nx - 1) mma_commit(&s.o_full[x]);
+        }
+        oc += j == nx - 1;
+      } else if (lane == 0) {
+        mbar_arrive(&s.slot_empty[slot]);
       }
+      if (++slot == kSlots) slot = 0, round ^= 1;
+      if (j + 1 < n) ok = key_item(j + 1 < nx, j + 2 == nx);
     }
-    if (++slot == kSlots) slot = 0, round ^= 1;
-    ++segs;
   }
   if (!ok && lane == 0) fail(s, p, where);
   // every MMA of this warp completes before Tensor Memory is released
@@ -274,12 +268,10 @@ __device__ void mma_issuer(Smem<D>& s, const AttnParams& p, const Share& sh) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Two warps: warp w takes column half w (d = 64: every other 4 rows).  They follow the ring item by item, so that they
-// never mistake one use of a slot for another.
+// Follows the ring item by item, so that it never mistakes one use of a slot for another.
 template <int D>
-__device__ void fixer(Smem<D>& s, const AttnParams& p, const Share& sh, int w) {
-  constexpr int kSlots = Smem<D>::kSlots;
-  constexpr int kGroups = D == 128 ? 32 : 16;  // groups of 4 rows of a warp
+__device__ void fixer(Smem<D>& s, const AttnParams& p, const Share& sh) {
+  constexpr int kSlots = Smem<D>::kSlots, kHalves = Smem<D>::kHalves;
   const int lane = threadIdx.x & 31;
   Segments<kKeys> walk(p, sh);
   Seg sg;
@@ -300,18 +292,16 @@ __device__ void fixer(Smem<D>& s, const AttnParams& p, const Share& sh, int w) {
           if (lane == 0) fail(s, p, 0xA21);
           return;
         }
-        if (kv == 1 && on_edge(p, u.pos0, last, u.held, key0)) {
-          char* v = reinterpret_cast<char*>(&s.kv[sl][D == 128 ? w : 0][0]) + lane * 16 + (D == 128 ? 0 : w * 512);
-          constexpr int kStep = D == 128 ? 512 : 1024;
-          const int row0 = (lane >> 3) + (D == 128 ? 0 : 4 * w);
+        if (kv == 1 && on_edge<kKeys>(p.window, p.sinks, u.pos0, last, u.held, key0)) {
+          // lane: 16 bytes of row 4 g + lane / 8 in each group g of 4 rows
+          char* v = reinterpret_cast<char*>(&s.kv[sl][0][0]) + lane * 16;
           uint32_t bad = 0;
 #pragma unroll 1
-          for (int g0 = 0; g0 < kGroups; g0 += 8) {
-            uint4 y[8];
+          for (int g0 = 0; g0 < 32; g0 += 4) {
             uint32_t dead = 0, look = 0;
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              const int key = key0 + row0 + (g0 + g) * (kStep / 128);
+            for (int g = 0; g < 4; ++g) {
+              const int key = key0 + 4 * (g0 + g) + (lane >> 3);
               const uint32_t first = key < p.sinks;
               const uint32_t d = (uint32_t)(key > hi) | ((uint32_t)(key < lo) & (first ^ 1u));
               const uint32_t full = (uint32_t)(key <= all) & ((uint32_t)(key >= from) | first);
@@ -319,22 +309,28 @@ __device__ void fixer(Smem<D>& s, const AttnParams& p, const Share& sh, int w) {
               look |= ((d | full) ^ 1u) << g;
             }
             if (__any_sync(0xffffffffu, look != 0)) {
+              uint4 y[4][kHalves];
 #pragma unroll
-              for (int g = 0; g < 8; ++g) y[g] = *reinterpret_cast<const uint4*>(v + (g0 + g) * kStep);
+              for (int g = 0; g < 4; ++g)
 #pragma unroll
-              for (int g = 0; g < 8; ++g) {
-                const uint32_t e[4] = {y[g].x, y[g].y, y[g].z, y[g].w};
-                uint32_t hit = 0;
+                for (int c = 0; c < kHalves; ++c)
+                  y[g][c] = *reinterpret_cast<const uint4*>(v + c * 128 * 128 + (g0 + g) * 512);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) hit |= (e[i] & 0x7f807f80u) + 0x00800080u;
-                // (an exponent of all ones carries into bit 15 or 31 when one is added to it)
+              for (int g = 0; g < 4; ++g) {
+                uint32_t hit = 0;  // (an exponent of all ones carries into bit 15 or 31 when one is added to it)
+#pragma unroll
+                for (int c = 0; c < kHalves; ++c)
+                  hit |= ((y[g][c].x & 0x7f807f80u) + 0x00800080u) | ((y[g][c].y & 0x7f807f80u) + 0x00800080u) |
+                         ((y[g][c].z & 0x7f807f80u) + 0x00800080u) | ((y[g][c].w & 0x7f807f80u) + 0x00800080u);
                 bad |= (look >> g & 1u) ? hit & 0x80008000u : 0u;
               }
             }
             if (__any_sync(0xffffffffu, dead != 0)) {
 #pragma unroll
-              for (int g = 0; g < 8; ++g)
-                if (dead >> g & 1u) *reinterpret_cast<uint4*>(v + (g0 + g) * kStep) = make_uint4(0, 0, 0, 0);
+              for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int c = 0; c < kHalves; ++c)
+                  if (dead >> g & 1u) *reinterpret_cast<uint4*>(v + c * 128 * 128 + (g0 + g) * 512) = make_uint4(0, 0, 0, 0);
             }
           }
           fence_proxy_async_smem();
@@ -366,15 +362,14 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// The 32 rows of a warp one by one (a lane per D / 32 columns): where values that are not finite would reach rows that
+// 32 rows of a tile one by one (a lane per D / 32 columns): where values that are not finite would reach rows that
 // do not see them.
 template <int D>
-__device__ __noinline__ void rows_one_by_one(const AttnParams& p, const Seg& sg, int x, int q4, bool whole, float* slot) {
+__device__ __noinline__ void rows_one_by_one(const AttnParams& p, const Seg& sg, int x, int row0, bool whole, float* slot) {
   constexpr int C = D / 32;
   const int lane = threadIdx.x & 31;
   const Unit& u = sg.u;
-  for (int i = 0; i < 32; ++i) {
-    const int r = 32 * q4 + i;
+  for (int r = row0; r < row0 + 32; ++r) {
     const int hh = (int)fast_div((uint32_t)r, p.by_tile_tokens);
     const int tok = x * p.tile_tokens + r - hh * p.tile_tokens;
     if (hh >= sg.heads || tok >= u.n) continue;
@@ -443,6 +438,37 @@ __device__ __noinline__ void join_rows(const AttnParams& p, const Seg& sg, int x
   const int hh0 = (int)fast_div((uint32_t)r0, p.by_tile_tokens);
   const bool mine = hh0 < sg.heads && x * p.tile_tokens + r0 - hh0 * p.tile_tokens < sg.u.n;
   const uint32_t mask = __ballot_sync(0xffffffffu, mine);
+  if (mask == 0xffffffffu) {
+    // a full warp: a lane per row, 32 columns of it at a time from two parts
+    const int at = 128 * x + r0, tok = x * p.tile_tokens + r0 - hh0 * p.tile_tokens;
+    __nv_bfloat16* o = (__nv_bfloat16*)p.o + (int64_t)(sg.h0 + hh0) * p.o_head + (int64_t)(sg.u.q0 + tok) * p.o_row;
+#pragma unroll 1
+    for (int g = 0; g < D / 32; ++g) {
+      float4 acc[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int c = first; c <= lastc; ++c) {
+        float* part = slot_ptr<D>(p, slot_of(c, first));
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part) + at);
+        const float w = ex2_approx(ml.x - own.x) * own.y;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float4 y = __ldcg(slot_out<D>(part, 8 * g + e, at));
+          acc[e].x = fmaf(w, y.x, acc[e].x);
+          acc[e].y = fmaf(w, y.y, acc[e].y);
+          acc[e].z = fmaf(w, y.z, acc[e].z);
+          acc[e].w = fmaf(w, y.w, acc[e].w);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<uint4*>(o + 32 * g + 8 * e) =
+            make_uint4(pack2(acc[2 * e].x, acc[2 * e].y), pack2(acc[2 * e].z, acc[2 * e].w),
+                       pack2(acc[2 * e + 1].x, acc[2 * e + 1].y), pack2(acc[2 * e + 1].z, acc[2 * e + 1].w));
+    }
+    return;
+  }
   const int n = __popc(mask);
   const int kth = (int)__fns(mask, 0, lane + 1);  // the lane-th row that exists
   for (int e0 = 0; e0 < n * (D / 4); e0 += 32) {
@@ -471,12 +497,10 @@ __device__ __noinline__ void join_rows(const AttnParams& p, const Seg& sg, int x
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
         const float w = ex2_approx(ml[b].x - mi.x) * mi.y;
-        // (a part without a key of this row left its outputs unwritten)
-        const bool none = ml[b].x == -INFINITY && ml[b].y == 0.f;
-        acc.x = none ? acc.x : fmaf(w, y[b].x, acc.x);
-        acc.y = none ? acc.y : fmaf(w, y[b].y, acc.y);
-        acc.z = none ? acc.z : fmaf(w, y[b].z, acc.z);
-        acc.w = none ? acc.w : fmaf(w, y[b].w, acc.w);
+        acc.x = fmaf(w, y[b].x, acc.x);
+        acc.y = fmaf(w, y[b].y, acc.y);
+        acc.z = fmaf(w, y[b].z, acc.z);
+        acc.w = fmaf(w, y[b].w, acc.w);
       }
     }
     __nv_bfloat16* o = (__nv_bfloat16*)p.o + (int64_t)(sg.h0 + hh) * p.o_head + (int64_t)(sg.u.q0 + tok) * p.o_row + 4 * c4;
@@ -484,34 +508,137 @@ __device__ __noinline__ void join_rows(const AttnParams& p, const Seg& sg, int x
   }
 }
 
-// P = 2^(a v + neg) as bf16 pairs into Tensor Memory, and the sum.  Of every 8 pairs, the first Poly take the polynomial
-// on the multiply-add pipe instead of the multi-function unit (which gives exactly 0 for a masked -infinity).
-template <int Poly>
-__device__ __forceinline__ void exponentials(const float (&v)[128], float a, float neg, uint32_t addr, float2 (&sum)[2]) {
-  const float2 a2 = make_float2(a, a), n2 = make_float2(neg, neg);
+// Columns of O multiplied by f.
+template <int N>
+__device__ __forceinline__ void rescale(uint32_t addr, float f) {
+#pragma unroll 1
+  for (int c = 0; c < N; c += 16) {
+    uint32_t o[16];
+    tmem_ld16(addr + c, o);
+    tmem_wait_ld();
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    uint32_t pk[32];
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float2 x = fma2(make_float2(v[64 * b + 2 * e], v[64 * b + 2 * e + 1]), a2, n2);
-      const float2 y = (e & 7) < Poly ? ex2_poly2(x) : make_float2(ex2_approx(x.x), ex2_approx(x.y));
-      sum[e & 1] = add2(sum[e & 1], y);
-      pk[e] = pack2(y.x, y.y);
+    for (int t = 0; t < 16; ++t) {
+      asm volatile("" : "+r"(o[t]));  // (not read in front of the wait)
+      o[t] = __float_as_uint(__uint_as_float(o[t]) * f);
     }
-    tmem_st32(addr + 32 * b, pk);
+    tmem_st16(addr + c, o);
   }
+  tmem_wait_st();
 }
 
-// Softmax warpgroup of tile x: S_x and P_x at Tensor Memory column 256 x, O_x at 256 x + 128.
+// A segment's softmax steps of one warp: what it needs, and nothing that the caller keeps across the segment (the call
+// boundary keeps that out of the loop's registers).
+struct Steps {
+  float a;
+  uint64_t wait_ns;
+  int window, sinks;
+  int x, n;                      // tile, key tiles
+  int first_pos, last_pos;       // of the tile's rows
+  int held, pos, last;           // rows the table covers; this row's position, the last row it sees
+  int tile, ahead, lo_t;         // first key tile; after `ahead` of them the list goes on at tile lo_t
+  uint32_t sc;                   // key tiles of this tile so far
+};
+
+// Scores at Tensor Memory column 256 x, P in the columns of scores that have been read.
+template <int D>
+__device__ __noinline__ bool softmax_steps(Smem<D>& s, const Steps t, float& ref_out, float& l_out) {
+  // (copies that no memory clobber makes the compiler read again)
+  const int x = t.x, steps = t.n, last = t.last, sinks = t.sinks, ahead = t.ahead, lo_t = t.lo_t;
+  const int win_lo = t.window > 0 && t.pos >= t.window ? t.pos - t.window + 1 : 0;  // the row's window
+  const int full_hi = min(t.first_pos, t.held - 1) - (kKeys - 1);                   // key tiles from here on: not every row sees all
+  const int past = t.window > 0 ? t.last_pos - t.window : -1;                       // key tiles up to here: neither ...
+  const int from = t.sinks - kKeys;                                                 // ... unless they come before that
+  const uint32_t sc = t.sc;
+  const uint64_t wait_ns = t.wait_ns;
+  const float a = t.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t s_addr = s.tmem_base + ((uint32_t)(32 * (warp & 3)) << 16) + 256 * x;
+  uint64_t* const s_full = &s.s_full[x];
+  uint64_t* const p_full = s.p_full[x];
+  float ref = -INFINITY;  // row reference (base 2)
+  float l = 0.f;          // row sum of 2^(x - ref)
+  int tile = t.tile;
+#pragma unroll 1
+  for (int j = 0; j < steps; ++j) {
+    const int key0 = tile * kKeys;
+    tile = j + 1 == ahead ? lo_t : tile + 1;
+    const bool edge = (key0 > full_hi) | ((key0 <= past) & (key0 > from));
+    if (!warp_wait(s_full, sc + j, &s.abort, wait_ns)) return false;
+    tc_fence_after();
+    uint32_t r[4][32];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, r[c]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_ld32_done(r[c]);
+    if (edge) {
+      const int hi = last + 1 - key0, lo = win_lo - key0, sk = sinks - key0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t seen = below(hi - 32 * c) & (~below(lo - 32 * c) | below(sk - 32 * c));
+#pragma unroll
+        for (int b = 0; b < 32; ++b) r[c][b] = (seen & (1u << b)) ? r[c][b] : 0xff800000u;
+      }
+    }
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int e = 0; e < 128; e += 8)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        mx[c] = max3_nan(mx[c], __uint_as_float(r[e >> 5][(e & 31) + 2 * c]), __uint_as_float(r[e >> 5][(e & 31) + 2 * c + 1]));
+    const float mt = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * a;
+    // The reference moves to the row maximum at the first finite score and whenever a score passes it by more than 2^8.
+    // (S(j) is complete, so P(j - 1) V_{j-1} in front of it is too, and O may be changed.)
+    const bool need = ref == -INFINITY ? mt > -INFINITY : mt - ref > kRescale;
+    if (__any_sync(0xffffffffu, need)) {
+      const float f = !need ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx(ref - mt));
+      if (j > 0) rescale<D>(s_addr + 128, f);
+      if (need) ref = mt;
+      l *= f;
+    }
+    const float neg = ref == -INFINITY ? 0.f : -ref;  // (a score of +infinity makes the row NaN)
+    const float2 a2 = make_float2(a, a), n2 = make_float2(neg, neg);
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    uint32_t pk[64];
+    auto exponentials = [&](int e0, int e1) {
+#pragma unroll
+      for (int e = e0; e < e1; ++e) {
+        const float2 y = fma2(make_float2(__uint_as_float(r[e >> 4][(2 * e) & 31]), __uint_as_float(r[e >> 4][(2 * e + 1) & 31])),
+                              a2, n2);
+        const float2 z = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+        sum[e & 1] = add2(sum[e & 1], z);
+        pk[e] = pack2(z.x, z.y);
+      }
+    };
+    auto hand_over = [&](int h) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[h]);
+    };
+    exponentials(0, 32);
+    tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+    exponentials(32, kLate);  // (while the stores are under way)
+    hand_over(0);
+    exponentials(kLate, 64);
+    tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+    sum[0] = add2(sum[0], sum[1]);
+    l += sum[0].x + sum[0].y;
+    hand_over(1);
+  }
+  ref_out = ref;
+  l_out = l;
+  return true;
+}
+
+// Softmax warpgroup of tile x: S_x and P_x at Tensor Memory column 256 x, O_x at 256 x + 128; a query row per thread.
 template <int D>
 __device__ void softmax_group(Smem<D>& s, const AttnParams& p, const Share& sh, int x) {
   const uint64_t wait_ns = 2 * p.wait_ns;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q4 = warp & 3;
   const int r = 32 * q4 + lane;  // row of the query tile
-  const uint32_t lane_addr = (uint32_t)(32 * q4) << 16;
-  const uint32_t s_addr = s.tmem_base + lane_addr + 256 * x, o_addr = s_addr + 128;
+  const uint32_t o_addr = s.tmem_base + ((uint32_t)(32 * q4) << 16) + 256 * x + 128;
   const int hh = (int)fast_div((uint32_t)r, p.by_tile_tokens);
   const int tok = x * p.tile_tokens + r - hh * p.tile_tokens;
   Segments<kKeys> walk(p, sh);
@@ -527,94 +654,19 @@ __device__ void softmax_group(Smem<D>& s, const AttnParams& p, const Share& sh, 
     const int first_pos = u.pos0 + x * p.tile_tokens;
     const int last_pos = u.pos0 + min((x + 1) * p.tile_tokens, u.n) - 1;
     const int nx = steps_of(p, sg, x);
-    float ref = -INFINITY;  // row reference (base 2)
-    float l = 0.f;          // row sum of 2^(x - ref)
-    for (int j = 0; j < nx; ++j, ++sc) {
-      if (!mbar_wait(&s.s_full[x], sc & 1, &s.abort, wait_ns)) {
-        fail(s, p, 0xA31);
-        return;
-      }
-      __syncwarp();
-      tc_fence_after();
-      uint32_t raw[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, raw[c]);
-      tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32_done(raw[c]);
-      float v[128];
-#pragma unroll
-      for (int e = 0; e < 128; ++e) v[e] = __uint_as_float(raw[e >> 5][e & 31]);
-      if (p.negate) {
-#pragma unroll
-        for (int e = 0; e < 128; ++e) v[e] = -v[e];
-      }
-      const int key0 = tile_of(u, sg.j0 + j) * kKeys;
-      const bool edge = on_edge(p, first_pos, last_pos, u.held, key0);
-      if (edge) {
-        const int hi = last - key0;                                                      // seen: up to hi ...
-        const int lo = p.window > 0 && pos >= p.window ? pos - p.window + 1 - key0 : 0;  // ... from lo on, or
-        const int sk = p.sinks - key0;                                                   // below sk
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t seen = (below(hi + 1 - 32 * c) & ~below(lo - 32 * c)) | (below(sk - 32 * c) & below(hi + 1 - 32 * c));
-#pragma unroll
-          for (int t = 0; t < 32; ++t) v[32 * c + t] = (seen & (1u << t)) ? v[32 * c + t] : -INFINITY;
-        }
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int e = 0; e < 128; e += 8)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mx[c] = max3_nan(mx[c], v[e + 2 * c], v[e + 2 * c + 1]);
-      const float mt = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * p.a;
-      // The reference (base 2) moves to the row maximum at the first finite score and whenever a score passes it by
-      // more than 2^8.  (S_x(j) is complete, so P_x(j - 1) V_{j-1} in front of it is too, and O_x may be changed.)
-      const bool need = ref == -INFINITY ? mt > -INFINITY : mt - ref > kRescale;
-      if (__any_sync(0xffffffffu, need)) {
-        const float f = !need ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx(ref - mt));
-        if (j > 0) {
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(o_addr + 32 * c, o);
-            tmem_wait_ld();
-            tmem_ld32_done(o);
-#pragma unroll
-            for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * f);
-            tmem_st32(o_addr + 32 * c, o);
-          }
-          tmem_wait_st();
-        }
-        if (need) ref = mt;
-        l *= f;
-      }
-      // (a score of NaN or +infinity makes the row NaN: the polynomial would not)
-      const float neg = !(mt < INFINITY) ? __int_as_float(0x7fffffff) : (ref == -INFINITY ? 0.f : -ref);
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      if (edge)
-        exponentials<0>(v, p.a, neg, s_addr, sum);
-      else
-        exponentials<kPoly>(v, p.a, neg, s_addr, sum);
-      sum[0] = add2(sum[0], sum[1]);
-      l += sum[0].x + sum[0].y;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.p_full[x]);
-    }
+    float ref = -INFINITY, l = 0.f;
+    if (nx > 0 && !softmax_steps<D>(s, Steps{p.a, wait_ns, p.window, p.sinks, x, nx, first_pos, last_pos, u.held, pos, last,
+                                   tile_of(u, sg.j0), u.ns - sg.j0, u.lo_t, sc},
+                          ref, l))
+      return fail(s, p, 0xA31);
+    sc += nx;
     if (nx > 0) {
-      if (!mbar_wait(&s.o_full[x], oc & 1, &s.abort, wait_ns)) {
-        fail(s, p, 0xA32);
-        return;
-      }
+      if (!warp_wait(&s.o_full[x], oc, &s.abort, wait_ns)) return fail(s, p, 0xA32);
       ++oc;
-      __syncwarp();
       tc_fence_after();
     }
     const bool slow = nx > 0 && *(volatile int*)&s.slow[segs % kSlowRing] == (int)segs + 1;
     const int row = u.q0 + tok, h = sg.h0 + hh;
-    __nv_bfloat16* orow = (__nv_bfloat16*)p.o + (int64_t)h * p.o_head + (int64_t)row * p.o_row;
     const int at = 128 * x + r;
     int first = 0, lastc = 0;
     float* slot = nullptr;
@@ -623,51 +675,55 @@ __device__ void softmax_group(Smem<D>& s, const AttnParams& p, const Share& sh, 
       slot = slot_ptr<D>(p, slot_of(blockIdx.x, first));
     }
     if (slow) {
-      rows_one_by_one<D>(p, sg, x, q4, whole, slot);
+      rows_one_by_one<D>(p, sg, x, 32 * q4, whole, slot);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.o_free[x]);
     } else {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      if (whole) {
-        if (row_ok && p.lse) p.lse[(int64_t)h * p.total_q + row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
-      } else {
-        __stcg(reinterpret_cast<float2*>(slot) + at, make_float2(ref, l));
-      }
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
+      uint32_t o[D / 32][32];
+      __syncwarp();
+      if (nx > 0) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) tmem_ld32(o_addr + 32 * c, o[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) tmem_ld32_done(o[c]);
+        tc_fence_before();
         __syncwarp();
-        if (nx > 0) {
-          tmem_ld32(o_addr + 32 * c, o);
-          tmem_wait_ld();
-          tmem_ld32_done(o);
-        } else {
+        if (lane == 0) mbar_arrive(&s.o_free[x]);
+      } else {
 #pragma unroll
-          for (int t = 0; t < 32; ++t) o[t] = 0;
-        }
-        if (!row_ok) continue;
-        if (whole) {
+        for (int e = 0; e < D; ++e) o[e >> 5][e & 31] = 0;
+      }
+      if (row_ok && whole) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (p.lse) p.lse[(int64_t)h * p.total_q + row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+        __nv_bfloat16* out = (__nv_bfloat16*)p.o + (int64_t)h * p.o_head + (int64_t)row * p.o_row;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint32_t q[4];
+        for (int g = 0; g < D / 8; ++g) {
+          uint32_t q[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              q[e] = pack2(__uint_as_float(o[8 * g + 2 * e]) * inv, __uint_as_float(o[8 * g + 2 * e + 1]) * inv);
-            *reinterpret_cast<uint4*>(orow + 32 * c + 8 * g) = make_uint4(q[0], q[1], q[2], q[3]);
+          for (int e = 0; e < 4; ++e) {
+            const int k = 8 * g + 2 * e;
+            q[e] = pack2(__uint_as_float(o[k >> 5][k & 31]) * inv, __uint_as_float(o[k >> 5][(k & 31) + 1]) * inv);
           }
-        } else {
+          *reinterpret_cast<uint4*>(out + 8 * g) = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+      } else if (row_ok) {
+        __stcg(reinterpret_cast<float2*>(slot) + at, make_float2(ref, l));
 #pragma unroll
-          for (int g = 0; g < 8; ++g)
-            __stcg(slot_out<D>(slot, 8 * c + g, at),
-                   make_float4(__uint_as_float(o[4 * g]), __uint_as_float(o[4 * g + 1]), __uint_as_float(o[4 * g + 2]),
-                               __uint_as_float(o[4 * g + 3])));
+        for (int g = 0; g < D / 4; ++g) {
+          const int k = 4 * g;
+          __stcg(slot_out<D>(slot, g, at),
+                 make_float4(__uint_as_float(o[k >> 5][k & 31]), __uint_as_float(o[k >> 5][(k & 31) + 1]),
+                             __uint_as_float(o[k >> 5][(k & 31) + 2]), __uint_as_float(o[k >> 5][(k & 31) + 3])));
         }
       }
     }
-    tc_fence_before();
-    if (!whole) __threadfence();
-    __syncwarp();
-    if (lane == 0 && nx > 0) mbar_arrive(&s.o_free[x]);
     if (whole) continue;
     // the CTA that comes last joins the unit's parts
+    __threadfence();
+    __syncwarp();
     if (lane == 0) mbar_arrive(&s.part_done);
     if (warp == kSoftmaxWarp0 && lane == 0) {
       if (!mbar_wait(&s.part_done, joins & 1, &s.abort, wait_ns)) {
@@ -679,10 +735,7 @@ __device__ void softmax_group(Smem<D>& s, const AttnParams& p, const Share& sh, 
       }
     }
     __syncwarp();
-    if (!mbar_wait(&s.join_go, joins & 1, &s.abort, wait_ns)) {
-      fail(s, p, 0xA34);
-      return;
-    }
+    if (!warp_wait(&s.join_go, joins, &s.abort, wait_ns)) return fail(s, p, 0xA34);
     const bool join = *(volatile int*)&s.join != 0;
     ++joins;
     if (!join) continue;
@@ -717,34 +770,38 @@ __device__ void softmax_group(Smem<D>& s, const AttnParams& p, const Share& sh, 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_tc(const __grid_constant__ Maps maps, const __grid_constant__ AttnParams p, int box_rows) {
-  extern __shared__ unsigned char smem_raw[];
-  Smem<D>& s = *reinterpret_cast<Smem<D>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  Smem<D>& s = *reinterpret_cast<Smem<D>*>(smem_raw);
+  if (smem_u32(smem_raw) & 1023u) {  // the swizzled tiles need it; there is no room to round up
+    set_status(p.ws, MR_ERR_DEVICE_CHECK, 0xA41);
+    return;
+  }
   empty_rows<__nv_bfloat16, D, kThreads>(p);
   Share sh;
   if (!make_share<kKeys, kThreads>(p, s.part, sh)) return;  // nothing for this CTA (all its threads leave)
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     mbar_init(&s.q_full, 1);
-    mbar_init(&s.q_empty, 1);
+    mbar_init(&s.q_empty, 2);
     for (int i = 0; i < Smem<D>::kSlots; ++i) {
       mbar_init(&s.slot_full[i], 1);
-      mbar_init(&s.slot_empty[i], 3);  // the MMAs that read it, and the fix-up warps
-      mbar_init(&s.slot_fixed[i], 2);
+      mbar_init(&s.slot_empty[i], 3);  // both tiles' MMAs, and the fix-up warp
+      mbar_init(&s.slot_fixed[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.p_full[i], 4);
+      for (int h = 0; h < 2; ++h) mbar_init(&s.p_full[i][h], 4);
       mbar_init(&s.o_full[i], 1);
       mbar_init(&s.o_free[i], 4);
     }
-    mbar_init(&s.part_done, 8);
+    mbar_init(&s.part_done, kSoftmaxWarps);
     mbar_init(&s.join_go, 1);
-    mbar_init(&s.mma_done, 1);
+    mbar_init(&s.mma_done, 2);
     s.abort = 0;
     for (int i = 0; i < kSlowRing; ++i) s.slow[i] = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kMmaWarp0) {
     tmem_alloc(&s.tmem_base, 512);
     tmem_relinquish();
   }
@@ -755,10 +812,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<kRegsControl>();
     if (warp == kProducerWarp)
       producer<D>(s, p, sh, maps, box_rows);
-    else if (warp == kMmaWarp)
-      mma_issuer<D>(s, p, sh);
+    else if (warp == kFixWarp)
+      fixer<D>(s, p, sh);
     else
-      fixer<D>(s, p, sh, warp - kFixWarp0);
+      mma_issuer<D>(s, p, sh, (warp - kMmaWarp0) >> 1);
   } else {
     regs_inc<kRegsSoftmax>();
     softmax_group<D>(s, p, sh, (warp - kSoftmaxWarp0) >> 2);
@@ -767,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(s.tmem_base, 512);
+  if (warp == kMmaWarp0) tmem_dealloc(s.tmem_base, 512);
 }
 
 template <int D>
@@ -778,7 +835,8 @@ cudaError_t launch(const Maps& maps, const AttnParams& p, int box_rows, int grid
   cudaError_t e = cudaFuncGetAttributes(&fa, k_attn_tc<D>);
   if (e != cudaSuccess) return e;
   if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  const size_t smem = sizeof(Smem<D>) + 1024;
+  constexpr size_t smem = sizeof(Smem<D>);
+  static_assert(smem <= 227 * 1024, "shared memory of a block");
   e = cudaFuncSetAttribute(k_attn_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   ProfScope ps(kKAttnTc, st);

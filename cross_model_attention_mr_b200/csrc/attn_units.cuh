@@ -24,7 +24,7 @@ struct AttnParams {
   FastDiv by_tile_tokens;
   int vec_q, vec_o;
   float a;                               // scale * log2(e)
-  int negate;                            // the products' sign is changed first (tensor-core kernel)
+  int negate;                            // the scores' sign is changed (tensor-core kernel: a stays positive)
   int window, sinks;
   int min_steps;                         // a CTA's share is at least this
   WsHeader* ws;

@@ -220,6 +220,15 @@ __device__ __forceinline__ void tmem_st2(uint32_t taddr, uint32_t a, uint32_t b)
   asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(a), "r"(b) : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 "
+      "[%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -306,22 +315,6 @@ __device__ __forceinline__ float ex2_poly(float x) {
   return x < -125.f ? 0.f : y;
 }
 
-// ex2_poly<5> of two values at once, for x <= 127: the same steps, two to an instruction; arguments below -126 give
-// 2^-126 instead of 0.
-__device__ __forceinline__ float2 ex2_poly2(float2 x) {
-  const float2 xc = make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
-  const float2 t = add2(xc, make_float2(12582912.f, 12582912.f));
-  const float2 r = add2(t, make_float2(-12582912.f, -12582912.f));
-  const float2 f = fma2(r, make_float2(-1.f, -1.f), xc);
-  float2 y = fma2(f, make_float2(0.00132764713f, 0.00132764713f), make_float2(0.00967554096f, 0.00967554096f));
-  y = fma2(y, f, make_float2(0.0555071309f, 0.0555071309f));
-  y = fma2(y, f, make_float2(0.240221202f, 0.240221202f));
-  y = fma2(y, f, make_float2(0.693146944f, 0.693146944f));
-  y = fma2(y, f, make_float2(1.00000012f, 1.00000012f));
-  return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(t.x) << 23)),
-                     __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
-}
-
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -353,6 +346,9 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
          ((uint32_t)(N >> 3) << 17)     // N / 8
          | ((uint32_t)(M >> 4) << 24);  // M / 16
 }
+
+// Set in an instruction descriptor: the product of -A.
+constexpr uint32_t kIdescNegateA = 1u << 13;
 
 // D[tmem] (+)= A[smem] * B[smem]^T, issued by one thread.
 __device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
