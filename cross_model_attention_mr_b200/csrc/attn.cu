@@ -358,7 +358,8 @@ cudaError_t launch_attn(const AttnArgs& a) {
   if (launch_attn_tc(a, p, sms, &e)) return e;
   attn_split(p, kRows, kMaxHeads);
   p.tokens = p.tile_tokens;
-  p.min_steps = 2;
+  p.unit_cost = 1;
+  p.min_steps = 3;
   if (a.dt == MR_BF16)
     return a.kv.d == 64 ? launch<__nv_bfloat16, 64>(p, sms, a.stream) : launch<__nv_bfloat16, 128>(p, sms, a.stream);
   return a.kv.d == 64 ? launch<float, 64>(p, sms, a.stream) : launch<float, 128>(p, sms, a.stream);

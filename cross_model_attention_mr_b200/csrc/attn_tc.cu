@@ -362,6 +362,18 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+// 32 bytes of a row: one store fills a sector of L2, two would write it in halves.
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&q)[8], bool aligned) {
+  if (aligned) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(q[0]), "r"(q[1]), "r"(q[2]),
+                 "r"(q[3]), "r"(q[4]), "r"(q[5]), "r"(q[6]), "r"(q[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(q[0], q[1], q[2], q[3]);
+    *(reinterpret_cast<uint4*>(dst) + 1) = make_uint4(q[4], q[5], q[6], q[7]);
+  }
+}
+
 // 32 rows of a tile one by one (a lane per D / 32 columns): where values that are not finite would reach rows that
 // do not see them.
 template <int D>
@@ -462,10 +474,15 @@ __device__ __noinline__ void join_rows(const AttnParams& p, const Seg& sg, int x
         }
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<uint4*>(o + 32 * g + 8 * e) =
-            make_uint4(pack2(acc[2 * e].x, acc[2 * e].y), pack2(acc[2 * e].z, acc[2 * e].w),
-                       pack2(acc[2 * e + 1].x, acc[2 * e + 1].y), pack2(acc[2 * e + 1].z, acc[2 * e + 1].w));
+      for (int e = 0; e < 8; e += 4) {
+        uint32_t q[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          q[2 * i] = pack2(acc[e + i].x, acc[e + i].y);
+          q[2 * i + 1] = pack2(acc[e + i].z, acc[e + i].w);
+        }
+        store32(o + 32 * g + 4 * e, q, p.vec_o == 2);
+      }
     }
     return;
   }
@@ -700,14 +717,14 @@ __device__ void softmax_group(Smem<D>& s, const AttnParams& p, const Share& sh, 
         if (p.lse) p.lse[(int64_t)h * p.total_q + row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
         __nv_bfloat16* out = (__nv_bfloat16*)p.o + (int64_t)h * p.o_head + (int64_t)row * p.o_row;
 #pragma unroll
-        for (int g = 0; g < D / 8; ++g) {
-          uint32_t q[4];
+        for (int g = 0; g < D / 16; ++g) {
+          uint32_t q[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = 8 * g + 2 * e;
+          for (int e = 0; e < 8; ++e) {
+            const int k = 16 * g + 2 * e;
             q[e] = pack2(__uint_as_float(o[k >> 5][k & 31]) * inv, __uint_as_float(o[k >> 5][(k & 31) + 1]) * inv);
           }
-          *reinterpret_cast<uint4*>(out + 8 * g) = make_uint4(q[0], q[1], q[2], q[3]);
+          store32(out + 16 * g, q, p.vec_o == 2);
         }
       } else if (row_ok) {
         __stcg(reinterpret_cast<float2*>(slot) + at, make_float2(ref, l));
@@ -852,7 +869,8 @@ bool launch_attn_tc(const AttnArgs& a, AttnParams p, int sms, cudaError_t* resul
   if (a.dt != MR_BF16 || a.kv.page_rows % 8 || !p.vec_q || !p.vec_o) return false;
   attn_split(p, 128, kMaxHeads);
   p.tokens = 2 * p.tile_tokens;
-  p.min_steps = 2;
+  p.unit_cost = 3;  // (about 7 us against 2.3 us for a key tile)
+  p.min_steps = 5;
   int box = 8;  // rows of a page that one copy takes
   while (box < kKeys && a.kv.page_rows % (2 * box) == 0) box *= 2;
   const int d = a.kv.d;
@@ -870,6 +888,7 @@ bool launch_attn_tc(const AttnArgs& a, AttnParams p, int sms, cudaError_t* resul
   // small that no score counts; masked ones stay -infinity)
   p.negate = p.a < 0.f;
   p.a = p.a == 0.f ? 1e-30f : fabsf(p.a);
+  if (((uintptr_t)a.o.ptr | (uintptr_t)(a.o.head_stride * 2) | (uintptr_t)(a.o.row_stride * 2)) % 32 == 0) p.vec_o = 2;
   p.wait_ns = kTimeoutNs;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   *result = d == 64 ? launch<64>(maps, p, box, grid, a.stream) : launch<128>(maps, p, box, grid, a.stream);

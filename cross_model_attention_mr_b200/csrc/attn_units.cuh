@@ -2,8 +2,8 @@
 //
 // A unit is (sequence, run of `tokens` new rows, kv head, chunk of `hp` query heads of its group); it reads a list of
 // key tiles of KT rows: the tiles that hold first rows kept visible, then those from the first window's start to the
-// last row's position.  All units' tiles, laid end to end (a run's heads next to one another), are one range of steps
-// that is split evenly over the CTAs: ragged batches, causal and windowed masks, and one long sequence with few new
+// last row's position.  All units' tiles, laid end to end (a run's heads next to one another, each with a few steps for
+// beginning and ending it), are one range of steps that is split evenly over the CTAs: ragged batches, causal and windowed masks, and one long sequence with few new
 // rows load the GPU alike.  A CTA's share may begin and end inside a unit; such parts are joined through the workspace
 // by the CTA that finishes last, in the order of the keys.  No CTA waits for another one.
 #pragma once
@@ -22,10 +22,11 @@ struct AttnParams {
   int total_q, H_q, group, chunks, hp;   // chunks of hp query heads per kv head (the last may be shorter)
   int tile_tokens, tokens;               // new rows of a tile of query rows, and of a unit
   FastDiv by_tile_tokens;
-  int vec_q, vec_o;
+  int vec_q, vec_o;                      // rows aligned to 16 bytes (vec_o 2: to 32)
   float a;                               // scale * log2(e)
   int negate;                            // the scores' sign is changed (tensor-core kernel: a stays positive)
   int window, sinks;
+  int unit_cost;                         // steps that beginning and ending a unit take
   int min_steps;                         // a CTA's share is at least this
   WsHeader* ws;
   uint32_t* counters;                    // one per CTA, zero at launch
@@ -71,6 +72,9 @@ __device__ __forceinline__ Unit make_unit(const AttnParams& p, int s, int r, int
   }
   return u;
 }
+
+// Steps of a unit: `unit_cost` in front for beginning and ending it, then its key tiles.
+__device__ __forceinline__ int cost_of(const AttnParams& p, const Unit& u) { return u.nk > 0 ? u.nk + p.unit_cost : 0; }
 
 // Entries of the unit's list that hold rows up to position hi.
 template <int KT>
@@ -120,7 +124,7 @@ __device__ bool make_share(const AttnParams& p, PartitionSmem& sm, Share& sh) {
   int64_t sum = 0;
   {
     Walk w;
-    for (int64_t i = tid; advance(w, i); i += NT) sum += make_unit<KT>(p, w.s, (int)(i - w.base), w.q0, w.n).nk;
+    for (int64_t i = tid; advance(w, i); i += NT) sum += cost_of(p, make_unit<KT>(p, w.s, (int)(i - w.base), w.q0, w.n));
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -140,8 +144,8 @@ __device__ bool make_share(const AttnParams& p, PartitionSmem& sm, Share& sh) {
   int64_t front = 0;  // steps per head in front of the NT runs looked at
   for (int64_t i = tid;; i += NT) {
     const bool live = advance(w, i);
-    const int nk = live ? make_unit<KT>(p, w.s, (int)(i - w.base), w.q0, w.n).nk : 0;
-    int64_t upto = nk;
+    const int cost = live ? cost_of(p, make_unit<KT>(p, w.s, (int)(i - w.base), w.q0, w.n)) : 0;
+    int64_t upto = cost;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
       const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
@@ -157,10 +161,10 @@ __device__ bool make_share(const AttnParams& p, PartitionSmem& sm, Share& sh) {
       if (v < warp) upto += sm.sums[v];
       all += sm.sums[v];
     }
-    if (live && sh.cur >= (upto - nk) * HC && sh.cur < upto * HC) {
+    if (live && sh.cur >= (upto - cost) * HC && sh.cur < upto * HC) {
       sm.s = w.s;
       sm.r = (int)(i - w.base);
-      sm.before = upto - nk;
+      sm.before = upto - cost;
     }
     front += all;
     if (sh.cur < front * HC) break;  // (cur < total: the runs end no earlier)
@@ -177,7 +181,7 @@ struct Seg {
   Unit u;
   int g, h0, heads;    // kv head, first query head, query heads
   int j0, j1;
-  int64_t first_step;  // of the unit
+  int64_t first_step;  // of the unit's key tiles, among all steps
 
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == u.nk; }
 };
@@ -196,33 +200,39 @@ struct Segments {
     u = make_unit<KT>(p, sh.s, sh.r, q0, n);
   }
   __device__ __forceinline__ bool next(Seg& sg) {
-    if (cur >= end) return false;
     const int64_t HC = (int64_t)p.kv.H_kv * p.chunks;
-    while (cur >= (before + u.nk) * HC) {  // to the next run that sees anything
-      before += u.nk;
-      int s = u.s, r = u.r + 1;
-      while (r >= runs_of(p, n)) {
-        seq_rows(p, ++s, q0, n);
-        r = 0;
+    while (cur < end) {
+      int cost = cost_of(p, u);
+      while (cur >= (before + cost) * HC) {  // to the next run that sees anything
+        before += cost;
+        int s = u.s, r = u.r + 1;
+        while (r >= runs_of(p, n)) {
+          seq_rows(p, ++s, q0, n);
+          r = 0;
+        }
+        u = make_unit<KT>(p, s, r, q0, n);
+        cost = cost_of(p, u);
       }
-      u = make_unit<KT>(p, s, r, q0, n);
+      const int64_t at = cur - before * HC;
+      const int hu = (int)(at / cost);
+      const int v0 = (int)(at - (int64_t)hu * cost), v1 = (int)min((int64_t)cost, v0 + (end - cur));
+      sg.first_step = cur - v0 + p.unit_cost;
+      cur += v1 - v0;
+      sg.j0 = max(v0 - p.unit_cost, 0);
+      sg.j1 = max(v1 - p.unit_cost, 0);
+      if (sg.j0 >= sg.j1) continue;  // none of the unit's tiles
+      sg.u = u;
+      sg.g = hu / p.chunks;
+      const int c = hu - sg.g * p.chunks;
+      sg.h0 = sg.g * p.group + c * p.hp;
+      sg.heads = min(p.hp, p.group - c * p.hp);
+      return true;
     }
-    const int64_t at = cur - before * HC;
-    const int hu = (int)(at / u.nk);
-    sg.u = u;
-    sg.j0 = (int)(at - (int64_t)hu * u.nk);
-    sg.j1 = (int)min((int64_t)u.nk, sg.j0 + (end - cur));
-    sg.g = hu / p.chunks;
-    const int c = hu - sg.g * p.chunks;
-    sg.h0 = sg.g * p.group + c * p.hp;
-    sg.heads = min(p.hp, p.group - c * p.hp);
-    sg.first_step = cur - sg.j0;
-    cur += sg.j1 - sg.j0;
-    return true;
+    return false;
   }
 };
 
-// CTAs that hold a unit's first and last step.
+// CTAs that hold a unit's first and last key tile.
 __device__ __forceinline__ void holders(const Share& sh, const Seg& sg, int& first, int& last) {
   first = (int)(((sg.first_step + 1) * sh.ctas - 1) / sh.total);
   last = (int)(((sg.first_step + sg.u.nk) * sh.ctas - 1) / sh.total);
