@@ -23,21 +23,4 @@ __device__ __forceinline__ int pool_row(const PagedKv& kv, int s, int g, int j) 
   return (page * kv.H_kv + g) * kv.page_rows + (j - pi * kv.page_rows);
 }
 
-// Sequence of packed row t: the s with cu[s] <= t < cu[s + 1], or n_seq when t is behind the last one.
-// Whole warp; cu ascends.  One round of 32 probes narrows the range 32-fold (a probe that finds
-// cu[i + 1] <= t leaves every sequence up to i behind).
-__device__ __forceinline__ int find_sequence(const int32_t* cu, int n_seq, int t, int lane) {
-  int lo = 0, hi = n_seq;  // the answer lies in [lo, hi]
-  while (hi > lo) {
-    const int step = (hi - lo + 31) / 32;
-    const int i = lo + (lane + 1) * step - 1;
-    const bool behind = i < hi && __ldg(cu + i + 1) <= t;
-    const int c = __popc(__ballot_sync(0xffffffffu, behind));
-    const int nlo = lo + c * step;
-    hi = min(hi, nlo + step - 1);
-    lo = min(nlo, hi);
-  }
-  return lo;
-}
-
 }  // namespace mr

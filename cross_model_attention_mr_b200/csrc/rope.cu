@@ -6,11 +6,12 @@
 // there).  The fraction goes to sincospi, whose argument needs no further reduction.  The rotation
 // itself is fp32 with one rounding to the tensor's type.
 //
-// Bound by memory: every element is read and written once, 3 operations each.  The sines cost far more than
-// that (some 40 instructions a pair), so a block takes up to kMaxTokens tokens, computes their table
-// once in shared memory, and uses it for every head of the query, key and (as a plain copy) value rows.
-// A unit of work is two 16-byte vectors: the two halves of 8 (fp32: 4) pairs in the half layout, or
-// neighbouring vectors in the interleaved one; the lanes of a warp cover whole rows.
+// Bound by memory: every element is read and written once, 3 operations each.  The sines cost more than that (some 30
+// instructions a pair), so a thread keeps one unit of a token, two 16-byte vectors, for several heads: the two halves of
+// 8 (fp32: 4) pairs in the half layout, or neighbouring vectors in the interleaved one.  Its loads do not depend on the
+// position, so they are under way while the position is looked up and the sines are computed; nothing is shared between
+// threads.  32 heads x 4096 rows of 128 in bf16: ROPE_US (a table of sines in shared memory, with the loads behind it:
+// 36 us).
 #include <cuda_bf16.h>
 
 #include "paged.cuh"
@@ -19,10 +20,8 @@
 namespace mr {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;    // tokens of a block
-constexpr int kMaxPairs = 128;   // rot_dim / 2
-constexpr int kUnroll = 4;       // units a thread loads before it stores the first
+constexpr int kThreads = 128;
+constexpr int kBatch = 4;  // heads whose rows a thread has under way
 
 template <typename T, int VEC>
 struct alignas(sizeof(T) * VEC) Vec {
@@ -40,121 +39,109 @@ struct Params {
   int n_rows, d, rot, interleaved;
   float mscale;
   int sign;              // -1 turns the other way
-  int tokens;            // tokens per block
   int heads_per_block;
   FastDiv by_units;      // units per row
-  FastDiv by_tokens;
   const int32_t* pos;    // rope: position of each row
   const int32_t* cu;     // append: row offsets, or NULL for one row per sequence
   PagedKv kv;
   WsHeader* ws;
 };
 
-// where a token's rows go
-struct Token {
-  int live;  // 0: leave everything alone; 1: rotate; 2: zero the query row, store nothing
-  int seq_row;  // position within the sequence (append)
-  int base;  // pool row of kv head 0, or -1: not stored
-};
+// Sequence of packed row t: the s with cu[s] <= t < cu[s + 1]; n_seq behind the last one, -1 in front of the first.
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int n_seq, int t) {
+  int lo = -1, hi = n_seq;  // cu[lo + 1] <= t or lo = -1; cu[hi] > t or hi = n_seq
+  while (hi - lo > 1) {
+    const int m = lo + (hi - lo) / 2;
+    if (__ldg(cu + m) <= t)
+      lo = m;
+    else
+      hi = m;
+  }
+  return lo < 0 ? -1 : (lo == n_seq - 1 && __ldg(cu + n_seq) <= t ? n_seq : lo);
+}
 
 template <typename T, int VEC, bool Append>
-__global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ mr_rope rope, const Params p) {
-  __shared__ float2 cs[kMaxTokens][kMaxPairs];
-  __shared__ Token tok[kMaxTokens];
-  __shared__ int tok_pos[kMaxTokens];
-  const int t0 = blockIdx.x * p.tokens;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nt = min(p.tokens, p.n_rows - t0);
-  if (warp < nt) {  // one warp per token of the block
-    const int t = t0 + warp;
-    Token k{1, 0, -1};
-    int at;
-    if (Append) {
-      const int s = p.cu ? find_sequence(p.cu, p.kv.n_seq, t, lane) : t;
-      k.live = 0;
-      at = 0;
-      // (a row in front of cu[0] belongs to no sequence)
-      if (s < p.kv.n_seq && (p.cu == nullptr || t >= __ldg(p.cu + s))) {
-        const int behind = p.cu ? __ldg(p.cu + s + 1) - t : 1;  // rows from this one to the sequence's last
-        const int64_t a = (int64_t)max(__ldg(p.kv.kv_len + s), 0) - behind;
-        at = (int)a;
-        k.live = a < 0 ? 2 : 1;
-        if (a >= 0) {
-          if (a < p.kv.capacity) {
-            k.base = pool_row(p.kv, s, 0, at);
-            if (k.base < 0 && lane == 0) set_status(p.ws, MR_ERR_DEVICE_CHECK, kBadPage);
-          } else if (lane == 0) {
-            set_status(p.ws, MR_ERR_DEVICE_CHECK, kTableShort);
-          }
-        }
-      }
-    } else {
-      at = __ldg(p.pos + t);
-    }
-    if (lane == 0) {
-      tok[warp] = k;
-      tok_pos[warp] = at;
-    }
-  }
-  __syncthreads();
-  const int half = p.rot >> 1;
-  for (int e = threadIdx.x; e < nt * half; e += kThreads) {
-    const int t = e / half, i = e - t * half;
-    const long long phase = (long long)((unsigned long long)(long long)tok_pos[t] * rope.turn[i]);
-    float s, c;
-    sincospif((float)phase * 1.0842021724855044e-19f, &s, &c);  // phase * 2^-63: half turns in [-1, 1]
-    cs[t][i] = make_float2(c * p.mscale, s * p.mscale * (float)p.sign);
-  }
-  __syncthreads();
-
-  const int upr = (int)p.by_units.d;
-  const int rotated = half / VEC;
-  const int h0 = blockIdx.y * p.heads_per_block;
-  const int all = p.heads[0] + p.heads[1] + p.heads[2];
-  const int n = min(p.heads_per_block, all - h0) * p.tokens * upr;
+__global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ mr_rope rope, const __grid_constant__ Params p) {
   using V = Vec<T, VEC>;
-  for (int u0 = threadIdx.x; u0 < n; u0 += kThreads * kUnroll) {
-    V a[kUnroll], b[kUnroll];
-    char* dst[kUnroll];  // NULL: nothing to do
-    int ia[kUnroll], ib[kUnroll], tt[kUnroll], ii[kUnroll];
+  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int upr = (int)p.by_units.d;
+  if (id >= (int64_t)p.n_rows * upr) return;
+  // (ids stay below 2^31 for the division: rows are taken in slabs of 2^20)
+  const int64_t slab = id / ((int64_t)upr << 20);
+  const int within = (int)(id - slab * ((int64_t)upr << 20));
+  const int t_in = (int)fast_div((uint32_t)within, p.by_units), i = within - t_in * upr;
+  const int t = (int)(slab << 20) + t_in;
+  const int half = p.rot >> 1, rotated = half / VEC;
+  // the unit's two vectors: the halves of its pairs, or neighbours
+  const bool split = i < rotated && !p.interleaved;
+  const int ia = split ? i * VEC : 2 * i * VEC, ib = split ? half + i * VEC : (2 * i + 1) * VEC;
+  const int all = p.heads[0] + p.heads[1] + p.heads[2];
+  const int h0 = blockIdx.y * p.heads_per_block, h1 = min(h0 + p.heads_per_block, all);
+
+  int live = 1, base = -1;  // live 0: leave everything alone; 1: rotate; 2: zero the query row, store nothing
+  bool known = false;
+  float c[VEC], s[VEC];
+  for (int hb = h0; hb < h1; hb += kBatch) {
+    V a[kBatch], b[kBatch];
 #pragma unroll
-    for (int w = 0; w < kUnroll; ++w) {
-      const int u = u0 + w * kThreads;
-      dst[w] = nullptr;
-      if (u >= n) continue;
-      const int row = (int)fast_div((uint32_t)u, p.by_units), i = u - row * upr;
-      int h = (int)fast_div((uint32_t)row, p.by_tokens);
-      const int t = row - h * p.tokens;
-      h += h0;
-      if (t >= nt || tok[t].live == 0) continue;
+    for (int w = 0; w < kBatch; ++w) {
+      int h = hb + w;
+      if (h >= h1) continue;
       const int kind = h < p.heads[0] ? 0 : h < p.heads[0] + p.heads[1] ? 1 : 2;
       h -= kind == 0 ? 0 : kind == 1 ? p.heads[0] : p.heads[0] + p.heads[1];
-      const char* src = p.src[kind].ptr + h * p.src[kind].head + (int64_t)(t0 + t) * p.src[kind].row;
-      if (Append && kind > 0) {
-        if (tok[t].base < 0) continue;
-        dst[w] = p.dst[kind].ptr + ((int64_t)tok[t].base + (int64_t)h * p.kv.page_rows) * p.d * (int)sizeof(T);
+      const char* src = p.src[kind].ptr + h * p.src[kind].head + (int64_t)t * p.src[kind].row;
+      a[w] = *reinterpret_cast<const V*>(src + ia * (int)sizeof(T));
+      b[w] = *reinterpret_cast<const V*>(src + ib * (int)sizeof(T));
+    }
+    if (!known) {  // (once: the rows above are under way)
+      known = true;
+      int at;
+      if (Append) {
+        const int seq = p.cu ? sequence_of(p.cu, p.kv.n_seq, t) : t;
+        live = 0;
+        at = 0;
+        if (seq >= 0 && seq < p.kv.n_seq) {
+          const int behind = p.cu ? __ldg(p.cu + seq + 1) - t : 1;  // rows from this one to the sequence's last
+          const int64_t q = (int64_t)max(__ldg(p.kv.kv_len + seq), 0) - behind;
+          at = (int)q;
+          live = q < 0 ? 2 : 1;
+          if (q >= p.kv.capacity) {
+            set_status(p.ws, MR_ERR_DEVICE_CHECK, kTableShort);
+          } else if (q >= 0) {
+            base = pool_row(p.kv, seq, 0, at);
+            if (base < 0) set_status(p.ws, MR_ERR_DEVICE_CHECK, kBadPage);
+          }
+        }
       } else {
-        dst[w] = p.dst[kind].ptr + h * p.dst[kind].head + (int64_t)(t0 + t) * p.dst[kind].row;
+        at = __ldg(p.pos + t);
       }
-      const bool turn = i < rotated && kind < 2;
-      // the unit's two vectors: the halves of its pairs, or neighbours
-      ia[w] = i < rotated && !p.interleaved ? i * VEC : 2 * i * VEC;
-      ib[w] = i < rotated && !p.interleaved ? half + i * VEC : (2 * i + 1) * VEC;
-      tt[w] = t;
-      ii[w] = turn ? i * VEC : -1;
-      if (Append && tok[t].live == 2) {
+      if (i < rotated) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) a[w].e[e] = b[w].e[e] = from_f32<T>(0.f);
-        ii[w] = -1;
-      } else {
-        a[w] = *reinterpret_cast<const V*>(src + ia[w] * (int)sizeof(T));
-        b[w] = *reinterpret_cast<const V*>(src + ib[w] * (int)sizeof(T));
+        for (int e = 0; e < VEC; ++e) {
+          const long long phase = (long long)((unsigned long long)(long long)at * rope.turn[i * VEC + e]);
+          sincospif((float)phase * 1.0842021724855044e-19f, &s[e], &c[e]);  // phase * 2^-63: half turns in [-1, 1]
+          c[e] *= p.mscale;
+          s[e] *= p.mscale * (float)p.sign;
+        }
       }
     }
 #pragma unroll
-    for (int w = 0; w < kUnroll; ++w) {
-      if (dst[w] == nullptr) continue;
-      if (ii[w] >= 0) {
+    for (int w = 0; w < kBatch; ++w) {
+      int h = hb + w;
+      if (h >= h1 || live == 0) continue;
+      const int kind = h < p.heads[0] ? 0 : h < p.heads[0] + p.heads[1] ? 1 : 2;
+      h -= kind == 0 ? 0 : kind == 1 ? p.heads[0] : p.heads[0] + p.heads[1];
+      char* dst;
+      if (Append && kind > 0) {
+        if (base < 0) continue;
+        dst = p.dst[kind].ptr + ((int64_t)base + (int64_t)h * p.kv.page_rows) * p.d * (int)sizeof(T);
+      } else {
+        dst = p.dst[kind].ptr + h * p.dst[kind].head + (int64_t)t * p.dst[kind].row;
+      }
+      if (Append && live == 2) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) a[w].e[e] = b[w].e[e] = from_f32<T>(0.f);
+      } else if (i < rotated && kind < 2) {
         if (p.interleaved) {  // 2 VEC consecutive elements hold VEC pairs
           float x[2 * VEC];
 #pragma unroll
@@ -164,8 +151,7 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ mr_ro
           }
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            const float2 r = cs[tt[w]][ii[w] + e];
-            const float y0 = x[2 * e] * r.x - x[2 * e + 1] * r.y, y1 = x[2 * e + 1] * r.x + x[2 * e] * r.y;
+            const float y0 = x[2 * e] * c[e] - x[2 * e + 1] * s[e], y1 = x[2 * e + 1] * c[e] + x[2 * e] * s[e];
             x[2 * e] = y0;
             x[2 * e + 1] = y1;
           }
@@ -177,15 +163,14 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ mr_ro
         } else {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            const float2 r = cs[tt[w]][ii[w] + e];
             const float x0 = to_f32<T>(a[w].e[e]), x1 = to_f32<T>(b[w].e[e]);
-            a[w].e[e] = from_f32<T>(x0 * r.x - x1 * r.y);
-            b[w].e[e] = from_f32<T>(x1 * r.x + x0 * r.y);
+            a[w].e[e] = from_f32<T>(x0 * c[e] - x1 * s[e]);
+            b[w].e[e] = from_f32<T>(x1 * c[e] + x0 * s[e]);
           }
         }
       }
-      *reinterpret_cast<V*>(dst[w] + ia[w] * (int)sizeof(T)) = a[w];
-      *reinterpret_cast<V*>(dst[w] + ib[w] * (int)sizeof(T)) = b[w];
+      *reinterpret_cast<V*>(dst + ia * (int)sizeof(T)) = a[w];
+      *reinterpret_cast<V*>(dst + ib * (int)sizeof(T)) = b[w];
     }
   }
 }
@@ -201,15 +186,12 @@ cudaError_t launch(const mr_rope* rope, Params& p, cudaStream_t st) {
   static const mr_rope none{};
   const int all = p.heads[0] + p.heads[1] + p.heads[2];
   p.by_units = make_fastdiv((uint32_t)(p.d / 2 / VEC));
-  // tokens per block: as many as leave two blocks for every SM; heads are split over blocks while there are
-  // still fewer blocks than that and a block keeps a full round of units
-  p.tokens = 1;
-  while (p.tokens < kMaxTokens && p.n_rows / (2 * p.tokens) >= 296) p.tokens *= 2;
-  p.by_tokens = make_fastdiv((uint32_t)p.tokens);
-  const int blocks = (p.n_rows + p.tokens - 1) / p.tokens;
-  int split = 1;
-  while (blocks * split < 296 && (all / (2 * split)) * p.tokens * (int)p.by_units.d >= kThreads) split *= 2;
-  p.heads_per_block = (all + split - 1) / split;
+  // heads of a thread: as many as leave about 8 blocks for every SM, a batch at least
+  const int64_t blocks = ((int64_t)p.n_rows * (p.d / 2 / VEC) + kThreads - 1) / kThreads;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  int batches = (all + kBatch - 1) / kBatch, each = 1;
+  while (each < batches && blocks * ((batches + 2 * each - 1) / (2 * each)) >= 8 * 148) each *= 2;
+  p.heads_per_block = each * kBatch;
   const dim3 grid((unsigned)blocks, (unsigned)((all + p.heads_per_block - 1) / p.heads_per_block));
   ProfScope ps(Append ? kKAppend : kKRope, st);
   k_rope<T, VEC, Append><<<grid, kThreads, 0, st>>>(rope ? *rope : none, p);

@@ -177,8 +177,13 @@ def fp8_scales_per_tile(block: int) -> int:
     return (block // 32) * (block // 64)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:  # (an eighth of the time of building a Stream object)
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -613,29 +618,38 @@ class BlockManager:
 _NO_SWITCH = contextlib.nullcontext()
 
 
-def _on_device_of(t: torch.Tensor):
-    """Context that makes the device of `t` current (the library launches on the current device)."""
-    if not t.is_cuda:
+def _on(t: torch.Tensor, stream):
+    """Context for a call on the tensors of t's device: that device is current (the library launches on the current
+    one), and `stream`, where given, is the current stream, so that outputs and workspaces made here belong to it."""
+    index = t.get_device()
+    if index < 0:
         raise ValueError("tensors must be CUDA tensors")
-    return _NO_SWITCH if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    if stream is None:
+        return _NO_SWITCH if index == torch.cuda.current_device() else torch.cuda.device(index)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=index) if stream else torch.cuda.default_stream(index)
+    if stream.device.index != index:
+        raise ValueError(f"the stream is not on {t.device}")
+    return torch.cuda.stream(stream)
 
 
 def _rows(t: torch.Tensor, like: torch.Tensor, what: str) -> Rows:
     """mr_rows of a [heads][rows][d] tensor with any strides over heads and rows."""
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+    stride = t.stride()
+    if len(stride) != 3 or (stride[2] != 1 and t.shape[2] > 1):
         raise ValueError(f"{what} must be [heads][rows][d] with adjacent elements in a row")
     if t.dtype != like.dtype:
         raise TypeError(f"{what} must have dtype {like.dtype}")
-    if t.device != like.device:
+    if t.get_device() != like.get_device():
         raise ValueError(f"{what} must be on {like.device}")
-    return Rows(t.data_ptr(), t.stride(0), t.stride(1))
+    return Rows(t.data_ptr(), stride[0], stride[1])
 
 
 def _ints(t: torch.Tensor, like: torch.Tensor, what: str, dim: int = 1) -> int:
     """Address of a contiguous int32 tensor on the device of `like`."""
-    if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.dim() != dim or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor of {dim} dimension(s)")
-    if t.device != like.device:
+    if t.get_device() != like.get_device():
         raise ValueError(f"{what} must be on {like.device}")
     return t.data_ptr()
 
@@ -669,7 +683,7 @@ def rope(r: Rope, X: torch.Tensor, pos: torch.Tensor, out: Optional[torch.Tensor
     """mr_rope_apply: X [H][rows][d] (any strides over heads and rows) rotated by each row's position
     (int32, device).  ``out=X`` rotates in place; ``adjoint=True`` gives the gradient with respect to X
     for a gradient with respect to the result."""
-    with _on_device_of(X):
+    with _on(X, stream):
         dt = _dt(X)
         x = _rows(X, X, "X")
         H, n, d = X.shape
@@ -682,7 +696,7 @@ def rope(r: Rope, X: torch.Tensor, pos: torch.Tensor, out: Optional[torch.Tensor
         elif out.shape != X.shape:
             raise ValueError("out must have the shape of X")
         check(LIB.mr_rope_apply(ctypes.byref(r.c), ctypes.byref(x), ctypes.byref(_rows(out, X, "out")), dt, H, n,
-                                _ints(pos, X, "pos"), 1 if adjoint else 0, _stream(stream)), "mr_rope_apply")
+                                _ints(pos, X, "pos"), 1 if adjoint else 0, _stream(None)), "mr_rope_apply")
     return out
 
 
@@ -704,6 +718,15 @@ class KVCache:
         return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device))
 
 
+def _ws_for(ws: Optional[Workspace], nbytes, t: torch.Tensor) -> Workspace:
+    """The caller's workspace (it must be on the device of t), or a new one of nbytes() bytes."""
+    if ws is None:
+        return Workspace(nbytes(), t.device)
+    if ws.buf.get_device() != t.get_device():
+        raise ValueError(f"the workspace must be on {t.device}")
+    return ws
+
+
 def _seqs(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor) -> KvSeqs:
     n = kv_len.shape[0]
     t, l = _ints(table, cache.k, "table", 2), _ints(kv_len, cache.k, "kv_len")
@@ -723,7 +746,7 @@ def kv_append(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, K: torc
     """mr_kv_append: store the new rows K, V [H_kv][total_q][d] (K rotated) in the pages that table
     [n_seq][pages_per_seq] names, ending at kv_len [n_seq], and return Q [H_q][total_q][d] rotated (None
     without Q; ``q_out=Q`` rotates in place).  ``cu_q`` [n_seq + 1]: rows of each sequence (None: one each)."""
-    with _on_device_of(cache.k):
+    with _on(cache.k, stream):
         k, v = _rows(K, cache.k, "K"), _rows(V, cache.k, "V")
         total = K.shape[1]
         if K.shape != V.shape or K.shape[0] != cache.H_kv or K.shape[2] != cache.d:
@@ -744,12 +767,11 @@ def kv_append(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, K: torc
         seqs = _seqs(cache, table, kv_len)
         if cu_q is not None and cu_q.shape[0] != seqs.n_seq + 1:
             raise ValueError("cu_q must have n_seq + 1 entries")
-        if ws is None:
-            ws = Workspace(paged_workspace_bytes(cache, cache.H_kv, seqs.n_seq), cache.k.device)
+        ws = _ws_for(ws, lambda: paged_workspace_bytes(cache, cache.H_kv, seqs.n_seq), cache.k)
         check(LIB.mr_kv_append(ctypes.byref(cache.c), ctypes.byref(seqs), ctypes.byref(rope.c) if rope else None, q, qo,
                                H_q, ctypes.byref(k), ctypes.byref(v),
                                _ints(cu_q, cache.k, "cu_q") if cu_q is not None else None, total, ws.ptr, ws.nbytes,
-                               _stream(stream)), "mr_kv_append")
+                               _stream(None)), "mr_kv_append")
     return q_out
 
 
@@ -776,19 +798,18 @@ def paged_decode(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, Q: t
     rows that table [n_seq][pages_per_seq] names -> O [H_q][n_seq][d], or (O, lse [H_q][n_seq]) with
     ``return_lse`` or an ``lse`` tensor.  ``window`` rows back and the first ``sinks`` rows are visible
     (window 0: all)."""
-    with _on_device_of(cache.k):
+    with _on(cache.k, stream):
         q = _rows(Q, cache.k, "Q")
         seqs = _seqs(cache, table, kv_len)
         H = Q.shape[0]
         if Q.shape[1] != seqs.n_seq or Q.shape[2] != cache.d:
             raise ValueError("Q must be [H_q][n_seq][d]")
         out, lse = _attn_out(Q, out, lse, return_lse)
-        if ws is None:
-            ws = Workspace(paged_workspace_bytes(cache, H, seqs.n_seq), cache.k.device)
+        ws = _ws_for(ws, lambda: paged_workspace_bytes(cache, H, seqs.n_seq), cache.k)
         check(LIB.mr_paged_decode(ctypes.byref(cache.c), ctypes.byref(seqs), ctypes.byref(q), H,
                                   1.0 / math.sqrt(cache.d) if scale is None else float(scale), int(window), int(sinks),
                                   ctypes.byref(_rows(out, cache.k, "out")), lse.data_ptr() if lse is not None else None,
-                                  ws.ptr, ws.nbytes, _stream(stream)), "mr_paged_decode")
+                                  ws.ptr, ws.nbytes, _stream(None)), "mr_paged_decode")
     return out if lse is None else (out, lse)
 
 
@@ -798,7 +819,7 @@ def paged_attn(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, Q: tor
     """mr_paged_attn: causal attention of the new rows Q [H_q][total_q][d] (rows cu_q[s] .. cu_q[s + 1] - 1 are the
     last ones of sequence s) over the cache -> O [H_q][total_q][d], or (O, lse [H_q][total_q]).  The rows' own keys
     and values must be in the cache (kv_append).  Rows behind cu_q[n_seq] are left as they are."""
-    with _on_device_of(cache.k):
+    with _on(cache.k, stream):
         q = _rows(Q, cache.k, "Q")
         seqs = _seqs(cache, table, kv_len)
         H, total = Q.shape[:2]
@@ -807,13 +828,12 @@ def paged_attn(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, Q: tor
         if cu_q.shape[0] != seqs.n_seq + 1:
             raise ValueError("cu_q must have n_seq + 1 entries")
         out, lse = _attn_out(Q, out, lse, return_lse)
-        if ws is None:
-            ws = Workspace(paged_workspace_bytes(cache, H, seqs.n_seq), cache.k.device)
+        ws = _ws_for(ws, lambda: paged_workspace_bytes(cache, H, seqs.n_seq), cache.k)
         check(LIB.mr_paged_attn(ctypes.byref(cache.c), ctypes.byref(seqs), ctypes.byref(q), H,
                                 _ints(cu_q, cache.k, "cu_q"), total,
                                 1.0 / math.sqrt(cache.d) if scale is None else float(scale), int(window), int(sinks),
                                 ctypes.byref(_rows(out, cache.k, "out")), lse.data_ptr() if lse is not None else None,
-                                ws.ptr, ws.nbytes, _stream(stream)), "mr_paged_attn")
+                                ws.ptr, ws.nbytes, _stream(None)), "mr_paged_attn")
     return out if lse is None else (out, lse)
 
 
@@ -825,7 +845,7 @@ def pages_copy(pools, pairs: torch.Tensor, ws: Optional[Workspace] = None, strea
     """mr_pages_copy: page pairs[t][1] <- page pairs[t][0] (int32, device) in every pool (tensors
     [n_pages][...], e.g. the k and v of every layer's cache)."""
     first = pools[0]
-    with _on_device_of(first):
+    with _on(first, stream):
         page_bytes = first.stride(0) * first.element_size()
         for t in pools:
             _need_cuda(t)
@@ -834,11 +854,10 @@ def pages_copy(pools, pairs: torch.Tensor, ws: Optional[Workspace] = None, strea
         p = _ints(pairs, first, "pairs", 2)
         if pairs.shape[1] != 2:
             raise ValueError("pairs must be [n][2]")
-        if ws is None:
-            ws = Workspace(pages_copy_workspace_bytes(), first.device)
+        ws = _ws_for(ws, pages_copy_workspace_bytes, first)
         ptrs = (_c_p * len(pools))(*[t.data_ptr() for t in pools])
         check(LIB.mr_pages_copy(ptrs, len(pools), page_bytes, first.shape[0], p, pairs.shape[0], ws.ptr, ws.nbytes,
-                                _stream(stream)), "mr_pages_copy")
+                                _stream(None)), "mr_pages_copy")
 
 
 class PagePool:

@@ -382,3 +382,30 @@ def test_attn_on_a_stream_and_in_a_graph(mr, dt):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, mr.paged_attn(cache, table, lens, q, c.cu))
+
+
+# ---------------------------------------------------------------------------------------------- streams that are given
+@pytest.mark.parametrize("handle", [False, True])
+def test_a_given_stream_without_a_workspace(mr, handle):
+    """Outputs and workspaces made inside a call belong to its stream: nothing on the current one can reuse them while
+    the call runs."""
+    c = Case(mr, [50, 3, 200], [50, 80, 900], 8, 2, 16, 128, "bf16", seed=13)
+    cache, table, lens, q = c.args()
+    want = mr.paged_attn(cache, table, lens, q, c.cu)
+    one = mr.paged_decode(cache, table, lens, q[:, :3].contiguous())
+    r = mr.Rope(128)
+    pos = torch.arange(c.T, dtype=torch.int32, device="cuda")
+    turned = mr.rope(r, q, pos)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    arg = st.cuda_stream if handle else st
+    torch.cuda.synchronize()
+    got = [mr.paged_attn(cache, table, lens, q, c.cu, stream=arg), mr.paged_decode(cache, table, lens, q[:, :3], stream=arg),
+           mr.rope(r, q, pos, stream=arg)]
+    junk = [torch.full((1 << 22,), math.nan, device="cuda") for _ in range(8)]
+    st.synchronize()
+    for g, w in zip(got, (want, one, turned)):
+        assert torch.equal(g, w)
+    del junk
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    assert torch.equal(mr.rope(r, q, pos, stream=0), turned)
