@@ -10,8 +10,9 @@
 // instructions a pair), so a thread keeps one unit of a token, two 16-byte vectors, for several heads: the two halves of
 // 8 (fp32: 4) pairs in the half layout, or neighbouring vectors in the interleaved one.  Its loads do not depend on the
 // position, so they are under way while the position is looked up and the sines are computed; nothing is shared between
-// threads.  32 heads x 4096 rows of 128 in bf16: ROPE_US (a table of sines in shared memory, with the loads behind it:
-// 36 us).
+// threads.  32 heads x 4096 rows of 128 in bf16: 10.9 us, 6.2 TB/s (a table of sines in shared memory, with the loads
+// behind it, took 36 us); appending 8192 rows of 28 + 2 x 4 heads: 33 us, 4.6 TB/s, as much as the same copies without
+// the sines.
 #include <cuda_bf16.h>
 
 #include "paged.cuh"
@@ -21,7 +22,7 @@ namespace mr {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kBatch = 4;  // heads whose rows a thread has under way
+constexpr int kMostHeads = 8;  // heads of a thread at most
 
 template <typename T, int VEC>
 struct alignas(sizeof(T) * VEC) Vec {
@@ -81,18 +82,12 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ mr_ro
   int live = 1, base = -1;  // live 0: leave everything alone; 1: rotate; 2: zero the query row, store nothing
   bool known = false;
   float c[VEC], s[VEC];
-  for (int hb = h0; hb < h1; hb += kBatch) {
-    V a[kBatch], b[kBatch];
-#pragma unroll
-    for (int w = 0; w < kBatch; ++w) {
-      int h = hb + w;
-      if (h >= h1) continue;
-      const int kind = h < p.heads[0] ? 0 : h < p.heads[0] + p.heads[1] ? 1 : 2;
-      h -= kind == 0 ? 0 : kind == 1 ? p.heads[0] : p.heads[0] + p.heads[1];
-      const char* src = p.src[kind].ptr + h * p.src[kind].head + (int64_t)t * p.src[kind].row;
-      a[w] = *reinterpret_cast<const V*>(src + ia * (int)sizeof(T));
-      b[w] = *reinterpret_cast<const V*>(src + ib * (int)sizeof(T));
-    }
+  for (int h = h0; h < h1; ++h) {
+    const int kind = h < p.heads[0] ? 0 : h < p.heads[0] + p.heads[1] ? 1 : 2;
+    const int hk = h - (kind == 0 ? 0 : kind == 1 ? p.heads[0] : p.heads[0] + p.heads[1]);
+    const char* src = p.src[kind].ptr + hk * p.src[kind].head + (int64_t)t * p.src[kind].row;
+    V a = *reinterpret_cast<const V*>(src + ia * (int)sizeof(T));
+    V b = *reinterpret_cast<const V*>(src + ib * (int)sizeof(T));
     if (!known) {  // (once: the rows above are under way)
       known = true;
       int at;
@@ -125,53 +120,47 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ mr_ro
         }
       }
     }
+    if (live == 0) continue;
+    char* dst;
+    if (Append && kind > 0) {
+      if (base < 0) continue;
+      dst = p.dst[kind].ptr + ((int64_t)base + (int64_t)hk * p.kv.page_rows) * p.d * (int)sizeof(T);
+    } else {
+      dst = p.dst[kind].ptr + hk * p.dst[kind].head + (int64_t)t * p.dst[kind].row;
+    }
+    if (Append && live == 2) {
 #pragma unroll
-    for (int w = 0; w < kBatch; ++w) {
-      int h = hb + w;
-      if (h >= h1 || live == 0) continue;
-      const int kind = h < p.heads[0] ? 0 : h < p.heads[0] + p.heads[1] ? 1 : 2;
-      h -= kind == 0 ? 0 : kind == 1 ? p.heads[0] : p.heads[0] + p.heads[1];
-      char* dst;
-      if (Append && kind > 0) {
-        if (base < 0) continue;
-        dst = p.dst[kind].ptr + ((int64_t)base + (int64_t)h * p.kv.page_rows) * p.d * (int)sizeof(T);
+      for (int e = 0; e < VEC; ++e) a.e[e] = b.e[e] = from_f32<T>(0.f);
+    } else if (i < rotated && kind < 2) {
+      if (p.interleaved) {  // 2 VEC consecutive elements hold VEC pairs
+        float x[2 * VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          x[e] = to_f32<T>(a.e[e]);
+          x[VEC + e] = to_f32<T>(b.e[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float y0 = x[2 * e] * c[e] - x[2 * e + 1] * s[e], y1 = x[2 * e + 1] * c[e] + x[2 * e] * s[e];
+          x[2 * e] = y0;
+          x[2 * e + 1] = y1;
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          a.e[e] = from_f32<T>(x[e]);
+          b.e[e] = from_f32<T>(x[VEC + e]);
+        }
       } else {
-        dst = p.dst[kind].ptr + h * p.dst[kind].head + (int64_t)t * p.dst[kind].row;
-      }
-      if (Append && live == 2) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) a[w].e[e] = b[w].e[e] = from_f32<T>(0.f);
-      } else if (i < rotated && kind < 2) {
-        if (p.interleaved) {  // 2 VEC consecutive elements hold VEC pairs
-          float x[2 * VEC];
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            x[e] = to_f32<T>(a[w].e[e]);
-            x[VEC + e] = to_f32<T>(b[w].e[e]);
-          }
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float y0 = x[2 * e] * c[e] - x[2 * e + 1] * s[e], y1 = x[2 * e + 1] * c[e] + x[2 * e] * s[e];
-            x[2 * e] = y0;
-            x[2 * e + 1] = y1;
-          }
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            a[w].e[e] = from_f32<T>(x[e]);
-            b[w].e[e] = from_f32<T>(x[VEC + e]);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float x0 = to_f32<T>(a[w].e[e]), x1 = to_f32<T>(b[w].e[e]);
-            a[w].e[e] = from_f32<T>(x0 * c[e] - x1 * s[e]);
-            b[w].e[e] = from_f32<T>(x1 * c[e] + x0 * s[e]);
-          }
+        for (int e = 0; e < VEC; ++e) {
+          const float x0 = to_f32<T>(a.e[e]), x1 = to_f32<T>(b.e[e]);
+          a.e[e] = from_f32<T>(x0 * c[e] - x1 * s[e]);
+          b.e[e] = from_f32<T>(x1 * c[e] + x0 * s[e]);
         }
       }
-      *reinterpret_cast<V*>(dst + ia * (int)sizeof(T)) = a[w];
-      *reinterpret_cast<V*>(dst + ib * (int)sizeof(T)) = b[w];
     }
+    *reinterpret_cast<V*>(dst + ia * (int)sizeof(T)) = a;
+    *reinterpret_cast<V*>(dst + ib * (int)sizeof(T)) = b;
   }
 }
 
@@ -186,13 +175,14 @@ cudaError_t launch(const mr_rope* rope, Params& p, cudaStream_t st) {
   static const mr_rope none{};
   const int all = p.heads[0] + p.heads[1] + p.heads[2];
   p.by_units = make_fastdiv((uint32_t)(p.d / 2 / VEC));
-  // heads of a thread: as many as leave about 8 blocks for every SM, a batch at least
+  // Heads of a thread: as many as leave 4 blocks for every SM, 8 at most.  (1024 blocks of 8 heads against 2048 of 4 for
+  // 4096 rows x 32 heads: 10.7 and 11.6 us; 16 and 32 heads for 8192 rows x 36: 33 and 43 us.)
   const int64_t blocks = ((int64_t)p.n_rows * (p.d / 2 / VEC) + kThreads - 1) / kThreads;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  int batches = (all + kBatch - 1) / kBatch, each = 1;
-  while (each < batches && blocks * ((batches + 2 * each - 1) / (2 * each)) >= 8 * 148) each *= 2;
-  p.heads_per_block = each * kBatch;
-  const dim3 grid((unsigned)blocks, (unsigned)((all + p.heads_per_block - 1) / p.heads_per_block));
+  int each = 1;
+  while (each < kMostHeads && blocks * ((all + 2 * each - 1) / (2 * each)) >= 4 * 148) each *= 2;
+  p.heads_per_block = each;
+  const dim3 grid((unsigned)blocks, (unsigned)((all + each - 1) / each));
   ProfScope ps(Append ? kKAppend : kKRope, st);
   k_rope<T, VEC, Append><<<grid, kThreads, 0, st>>>(rope ? *rope : none, p);
   return cudaGetLastError();
