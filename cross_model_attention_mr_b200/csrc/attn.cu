@@ -30,27 +30,22 @@ struct Smem {
   float q[kRows * kStride];
   float k[kKeys * kStride];                   // the probabilities take its place
   float v[kKeys * D];
+  int rows[2][kKeys];                         // pool rows of this key tile and the next one (-1: zeros)
   PartitionSmem part;
   int last;
 };
 static_assert(Smem<64>::kPStride * kRows <= kKeys * Smem<64>::kStride, "probabilities fit");
 
-// `live` rows of K or V from the pool into shared memory as fp32; the others become zeros.
+// Rows of K or V from the pool into shared memory as fp32; rows[] < 0 become zeros.
 template <typename T, int D>
-__device__ __forceinline__ void load_rows(const AttnParams& p, const Seg& sg, const void* pool, int key0, int lo, int hi,
-                                          float* dst, int stride) {
+__device__ __forceinline__ void load_rows(const void* pool, const int* rows, float* dst, int stride) {
   constexpr int V = 16 / sizeof(T);            // elements of a 16-byte load
   constexpr int kVecs = kKeys * (D / V);
 #pragma unroll 4
   for (int e = threadIdx.x; e < kVecs; e += kThreads) {
     const int r = e / (D / V), c = (e % (D / V)) * V;
-    const int j = key0 + r;
     float* d = dst + r * stride + c;
-    int row = -1;
-    if (j <= hi && (j >= lo || j < p.sinks)) {
-      row = pool_row(p.kv, sg.u.s, sg.g, j);
-      if (row < 0) set_status(p.ws, MR_ERR_DEVICE_CHECK, kBadPage);
-    }
+    const int row = rows[r];
     const T* src = (const T*)pool + (int64_t)max(row, 0) * D + c;
     if constexpr (sizeof(T) == 4) {
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(d)), "l"(src), "r"(row >= 0 ? 16 : 0)
@@ -123,13 +118,26 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(const AttnParams p) {
   while (walk.next(sg)) {
     const Unit& u = sg.u;
     // query rows: head r / tile_tokens, new row r % tile_tokens
-    for (int e = threadIdx.x; e < kRows * D; e += kThreads) {
-      const int r = e / D, c = e % D;
+    const auto query = [&](int r, int c) -> const T* {  // NULL: a row that does not exist
       const int hh = (int)fast_div((uint32_t)r, p.by_tile_tokens), t = r - hh * p.tile_tokens;
-      s.q[r * kStride + c] =
-          hh < sg.heads && t < u.n
-              ? to_f32<T>(((const T*)p.q)[(int64_t)(sg.h0 + hh) * p.q_head + (int64_t)(u.q0 + t) * p.q_row + c])
-              : 0.f;
+      return hh < sg.heads && t < u.n
+                 ? (const T*)p.q + (int64_t)(sg.h0 + hh) * p.q_head + (int64_t)(u.q0 + t) * p.q_row + c
+                 : nullptr;
+    };
+    if (sizeof(T) == 4 && p.vec_q) {
+#pragma unroll
+      for (int e = threadIdx.x; e < kRows * D / 4; e += kThreads) {
+        const int r = e / (D / 4), c = 4 * (e % (D / 4));
+        const T* x = query(r, c);
+        *reinterpret_cast<float4*>(s.q + r * kStride + c) =
+            x ? *reinterpret_cast<const float4*>(x) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    } else {
+#pragma unroll 8
+      for (int e = threadIdx.x; e < kRows * D; e += kThreads) {
+        const T* x = query(e / D, e % D);
+        s.q[e / D * kStride + e % D] = x ? to_f32<T>(*x) : 0.f;
+      }
     }
     int hh[4], tok[4], pos[4], last[4];  // of this thread's rows: head, new row (-1: none), position, last row seen
     float m[4], l[4], acc[4][D / 16];
@@ -149,12 +157,24 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(const AttnParams p) {
     const int hi = min(u.pos0 + u.n - 1, u.held - 1);
     const int lo = p.window > 0 && u.pos0 >= p.window ? u.pos0 - p.window + 1 : 0;
     const int pos_last = u.pos0 + u.n - 1;
+    // pool row of key tile j's key threadIdx.x, or -1 where no row of the unit sees it
+    auto lookup = [&](int j) {
+      const int key = tile_of(u, j) * kKeys + (int)threadIdx.x;
+      if (threadIdx.x >= kKeys || j >= sg.j1 || key > hi || (key < lo && key >= p.sinks)) return -1;
+      const int row = pool_row(p.kv, u.s, sg.g, key);
+      if (row < 0) set_status(p.ws, MR_ERR_DEVICE_CHECK, kBadPage);
+      return row;
+    };
+    if (threadIdx.x < kKeys) s.rows[0][threadIdx.x] = lookup(sg.j0);
+    __syncthreads();
     for (int j = sg.j0; j < sg.j1; ++j) {
-      const int key0 = tile_of(u, j) * kKeys;
-      load_rows<T, D>(p, sg, p.kv.k, key0, lo, hi, s.k, kStride);
+      const int key0 = tile_of(u, j) * kKeys, buf = (j - sg.j0) & 1;
+      load_rows<T, D>(p.kv.k, s.rows[buf], s.k, kStride);
       asm volatile("cp.async.commit_group;" ::: "memory");
-      load_rows<T, D>(p, sg, p.kv.v, key0, lo, hi, s.v, D);
+      load_rows<T, D>(p.kv.v, s.rows[buf], s.v, D);
       asm volatile("cp.async.commit_group;" ::: "memory");
+      const int next = lookup(j + 1);  // (the table is read while the rows are under way)
+      if (threadIdx.x < kKeys) s.rows[buf ^ 1][threadIdx.x] = next;
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncthreads();
       float x[4][4];
@@ -252,31 +272,48 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(const AttnParams p) {
       finish = s.last != 0;
       if (finish) {
         __threadfence();
+        // the thread's four rows together, part by part in the order of the keys
+        float top[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = 4 * ty + i;
-          m[i] = -INFINITY;
-          for (int c = first; c <= lastc; ++c)
-            m[i] = fmaxf(m[i], __ldcg(reinterpret_cast<const float2*>(p.part + slot_of(c, first) * kSlot) + r).x);
-          const float ref = m[i] == -INFINITY ? 0.f : m[i];
+          top[i] = -INFINITY;
           l[i] = 0.f;
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
-          for (int b = first; b <= lastc; ++b) {
-            const float* part = p.part + slot_of(b, first) * kSlot;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part) + r);
-            const float w = ex2_approx(ml.x - ref);
-            l[i] = fmaf(w, ml.y, l[i]);
+        }
+#pragma unroll 2
+        for (int b = first; b <= lastc; ++b) {
+          const float2* ml = reinterpret_cast<const float2*>(p.part + slot_of(b, first) * kSlot) + 4 * ty;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], __ldcg(ml + i).x);
+        }
+#pragma unroll 2
+        for (int b = first; b <= lastc; ++b) {
+          const float* part = p.part + slot_of(b, first) * kSlot;
+          float2 ml[4];
+          float4 y[4][D / 64];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            ml[i] = __ldcg(reinterpret_cast<const float2*>(part) + 4 * ty + i);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              y[i][c] = __ldcg(reinterpret_cast<const float4*>(part + 2 * kRows + (4 * ty + i) * D + 4 * tx + 64 * c));
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float w = ex2_approx(ml[i].x - (top[i] == -INFINITY ? 0.f : top[i]));
+            l[i] = fmaf(w, ml[i].y, l[i]);
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
-              const float4 y = __ldcg(reinterpret_cast<const float4*>(part + 2 * kRows + r * D + 4 * tx + 64 * c));
-              acc[i][4 * c] = fmaf(w, y.x, acc[i][4 * c]);
-              acc[i][4 * c + 1] = fmaf(w, y.y, acc[i][4 * c + 1]);
-              acc[i][4 * c + 2] = fmaf(w, y.z, acc[i][4 * c + 2]);
-              acc[i][4 * c + 3] = fmaf(w, y.w, acc[i][4 * c + 3]);
+              acc[i][4 * c] = fmaf(w, y[i][c].x, acc[i][4 * c]);
+              acc[i][4 * c + 1] = fmaf(w, y[i][c].y, acc[i][4 * c + 1]);
+              acc[i][4 * c + 2] = fmaf(w, y[i][c].z, acc[i][4 * c + 2]);
+              acc[i][4 * c + 3] = fmaf(w, y[i][c].w, acc[i][4 * c + 3]);
             }
           }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = top[i];
       }
     }
     if (finish) {
@@ -359,7 +396,8 @@ cudaError_t launch_attn(const AttnArgs& a) {
   attn_split(p, kRows, kMaxHeads);
   p.tokens = p.tile_tokens;
   p.unit_cost = 1;
-  p.min_steps = 3;
+  p.min_steps = 1;
+  p.max_parts = 24;
   if (a.dt == MR_BF16)
     return a.kv.d == 64 ? launch<__nv_bfloat16, 64>(p, sms, a.stream) : launch<__nv_bfloat16, 128>(p, sms, a.stream);
   return a.kv.d == 64 ? launch<float, 64>(p, sms, a.stream) : launch<float, 128>(p, sms, a.stream);

@@ -870,7 +870,8 @@ bool launch_attn_tc(const AttnArgs& a, AttnParams p, int sms, cudaError_t* resul
   attn_split(p, 128, kMaxHeads);
   p.tokens = 2 * p.tile_tokens;
   p.unit_cost = 3;  // (about 7 us against 2.3 us for a key tile)
-  p.min_steps = 5;
+  p.min_steps = 4;
+  p.max_parts = 24;
   int box = 8;  // rows of a page that one copy takes
   while (box < kKeys && a.kv.page_rows % (2 * box) == 0) box *= 2;
   const int d = a.kv.d;

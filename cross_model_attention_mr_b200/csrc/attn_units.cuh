@@ -27,7 +27,8 @@ struct AttnParams {
   int negate;                            // the scores' sign is changed (tensor-core kernel: a stays positive)
   int window, sinks;
   int unit_cost;                         // steps that beginning and ending a unit take
-  int min_steps;                         // a CTA's share is at least this
+  int min_steps;                         // a CTA's share is at least this ...
+  int max_parts;                         // ... and no unit has many more parts than this
   WsHeader* ws;
   uint32_t* counters;                    // one per CTA, zero at launch
   float* part;                           // two slots per CTA
@@ -96,6 +97,7 @@ struct Share {
 
 struct PartitionSmem {
   int64_t sums[32];
+  int most[32];
   int64_t before;
   int s, r;
 };
@@ -122,21 +124,36 @@ __device__ bool make_share(const AttnParams& p, PartitionSmem& sm, Share& sh) {
     return w.s < n_seq;
   };
   int64_t sum = 0;
+  int most = 0;
   {
     Walk w;
-    for (int64_t i = tid; advance(w, i); i += NT) sum += cost_of(p, make_unit<KT>(p, w.s, (int)(i - w.base), w.q0, w.n));
+    for (int64_t i = tid; advance(w, i); i += NT) {
+      const int cost = cost_of(p, make_unit<KT>(p, w.s, (int)(i - w.base), w.q0, w.n));
+      sum += cost;
+      most = max(most, cost);
+    }
   }
 #pragma unroll
-  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  if (lane == 0) sm.sums[warp] = sum;
+  for (int d = 16; d; d >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+  }
+  if (lane == 0) {
+    sm.sums[warp] = sum;
+    sm.most[warp] = most;
+  }
   __syncthreads();
   int64_t steps = 0;
 #pragma unroll
-  for (int i = 0; i < NT / 32; ++i) steps += sm.sums[i];
+  for (int i = 0; i < NT / 32; ++i) {
+    steps += sm.sums[i];
+    most = max(most, sm.most[i]);
+  }
   const int64_t HC = (int64_t)p.kv.H_kv * p.chunks;
   sh.total = steps * HC;
   const int64_t k = blockIdx.x;
-  sh.ctas = min((int64_t)gridDim.x, (sh.total + p.min_steps - 1) / p.min_steps);
+  const int64_t least = max(p.min_steps, (most + p.max_parts - 1) / p.max_parts);
+  sh.ctas = min((int64_t)gridDim.x, (sh.total + least - 1) / least);
   if (k >= sh.ctas) return false;
   sh.cur = k * sh.total / sh.ctas;
   sh.end = (k + 1) * sh.total / sh.ctas;
