@@ -5,11 +5,12 @@
 // tile serves the whole group, and one persistent CTA per SM walks its share of the units' key tiles (attn_units.cuh).
 // Tensor Memory holds S and O of both tiles; P takes the place of S.
 //   * producer warp: TMA loads of the query tiles (a box of rows x heads) and of key and value tiles page by page (a
-//     lane per box; what nobody sees is asked for outside the pool, which TMA fills with zeros), K_0, V_0, K_1, ...
-//     through a ring;
-//   * an MMA warp for each tile: S(0) = Q K_0^T, then for each key tile j O += P(j) V_j, in two halves as P is handed
-//     over, and S(j + 1) behind it, so one tile's products run during the other one's softmax.  S, P and O of a tile are
-//     ordered by the tensor core's own order, so no barrier says that P has been read;
+//     lane per box; what nobody sees is asked for outside the pool, which TMA fills with zeros), K_0, K_1,
+//     V_0, K_2, V_1, ... through a ring;
+//   * an MMA warp for each tile.  The scores of a key tile come in two halves of 64 keys: S_1(j + 1) takes the place of
+//     S_1(j) as soon as the softmax has read that, S_0(j + 1) the place of S_0(j) and P(j) behind O += P(j) V_j.  So the
+//     softmax works on one half while the products that the other half waits for run.  S, P and O of a tile are ordered
+//     by the tensor core's own order, so no barrier says that P has been read;
 //   * two softmax warpgroups, a query row per thread: the mask only where some row does not see some key, a row reference
 //     that moves when a score passes it by 2^8 (O is then rescaled in Tensor Memory), P = 2^(x - reference) in bf16;
 //   * a fix-up warp looks after the values of key tiles that not every row sees: rows that nobody of the unit sees become
@@ -43,13 +44,12 @@ constexpr int kRegsControl = 72;
 constexpr int kRegsSoftmax = 216;
 static_assert(kRegsControl + 2 * kRegsSoftmax == 3 * kLaunchRegs, "register split");
 constexpr int kKeys = 128;
-constexpr int kHalf = 64;         // keys whose P is handed over at a time
+constexpr int kHalf = 64;         // keys whose scores and P are handed over at a time
 constexpr int kMaxHeads = 32;     // query heads of a tile at most
 constexpr int kMaxCtas = 152;     // one per SM
 constexpr int kSlowRing = 16;     // segments that can be under way at once, and more
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr float kRescale = 8.0f;
-constexpr int kLate = 40;         // pairs of exponentials before the first half of P is handed over
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
@@ -61,7 +61,8 @@ struct Smem {
   __nv_bfloat16 kv[kSlots][kHalves][128 * 64];   // [slot][column half][key][64]
   uint64_t q_full, q_empty;
   uint64_t slot_full[kSlots], slot_empty[kSlots], slot_fixed[kSlots];
-  uint64_t s_full[2], p_full[2][2];              // [tile], [tile][key half]
+  uint64_t s_full[2][2], p_full[2][2];           // [tile][key half]
+  uint64_t s_read[2];                            // the second half's scores are in registers
   uint64_t o_full[2], o_free[2];
   uint64_t part_done, join_go, mma_done;
   PartitionSmem part;
@@ -139,15 +140,18 @@ __device__ void producer(Smem<D>& s, const AttnParams& p, const Share& sh, const
       if (r < 0) set_status(p.ws, MR_ERR_DEVICE_CHECK, kBadPage);
       return r < 0 ? nowhere : r;
     };
-    int row = lookup(sg.j0);
-    for (int j = sg.j0; j < sg.j1 && ok; ++j) {
-      const int next_row = lookup(j + 1);
-      for (int kv = 0; kv < 2; ++kv, ++item) {
+    // K_0, then K_{j+1} and V_j for each j
+    int row = lookup(sg.j0), next_row = row;
+    for (int j = sg.j0 - 1; j < sg.j1 && ok; ++j) {
+      for (int kv = 0; kv < 2; ++kv) {
+        if (kv == 0 ? j + 1 >= sg.j1 : j < sg.j0) continue;
         const int sl = item % kSlots;
         const uint32_t use = item / kSlots;
+        ++item;
         if (use > 0) ok = mbar_wait_sleep(&s.slot_empty[sl], (use - 1) & 1, &s.abort, p.wait_ns, 64);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
+          --item;
           if (lane == 0) fail(s, p, 0xA02);
           break;
         }
@@ -155,9 +159,11 @@ __device__ void producer(Smem<D>& s, const AttnParams& p, const Share& sh, const
         __syncwarp();
         if (lane < boxes)
           for (int c = 0; c < kHalves; ++c)
-            tma_load_2d(&s.kv[sl][c][lane * box_rows * 64], kv ? &maps.v : &maps.k, &s.slot_full[sl], 64 * c, row);
+            tma_load_2d(&s.kv[sl][c][lane * box_rows * 64], kv ? &maps.v : &maps.k, &s.slot_full[sl], 64 * c,
+                        kv ? row : next_row);
       }
       row = next_row;
+      next_row = lookup(j + 2);
     }
   }
   // no load may land after the CTA releases its shared memory
@@ -177,7 +183,7 @@ template <int D>
 __device__ void mma_issuer(Smem<D>& s, const AttnParams& p, const Share& sh, int x) {
   constexpr int kSlots = Smem<D>::kSlots;
   constexpr uint32_t kSlotLo = Smem<D>::kSlotBytes >> 4;  // a slot further, in a descriptor's low word
-  const uint32_t id_qk = idesc_bf16_f32(128, kKeys, false, false) | (p.negate ? kIdescNegateA : 0u);
+  const uint32_t id_qk = idesc_bf16_f32(128, kHalf, false, false) | (p.negate ? kIdescNegateA : 0u);
   constexpr uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
   const int lane = threadIdx.x & 31;
   const uint32_t s_col = __shfl_sync(0xffffffffu, s.tmem_base, 0) + 256 * x, o_col = s_col + 128;
@@ -190,33 +196,32 @@ __device__ void mma_issuer(Smem<D>& s, const AttnParams& p, const Share& sh, int
   Seg sg;
   uint32_t segs = 0, fixed = 0;        // fixed: a parity bit per slot
   uint32_t slot = 0, round = 0;        // ring position of the next item, and its use's parity
-  uint32_t pc = 0, oc = 0, where = 0;  // P tiles and outputs so far
+  uint32_t pc = 0, oc = 0, where = 0;  // steps (P tiles) and outputs so far
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
     const bool ok = warp_wait(bar, parity, &s.abort, p.wait_ns);
     if (!ok) where = code;
     return ok;
   };
-  // S = Q K^T of the item at hand (or nothing), which is then passed on
-  auto key_item = [&](bool use, bool last) {
-    if (!wait(&s.slot_full[slot], round, 0xA12)) return false;
-    if (use) {
-      tc_fence_after();
-      const uint64_t kd = k_desc + slot * kSlotLo;
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * 128 * 128 + 32 * (kk & 3)) >> 4;
-          mma_bf16_ss(s_col, q_desc + off, kd + off, id_qk, kk > 0 ? 1u : 0u);
-        }
-        mma_commit(&s.s_full[x]);
-        mma_commit(&s.slot_empty[slot]);
-        if (last) mma_commit(&s.q_empty);
-      }
-    } else if (lane == 0) {
-      mbar_arrive(&s.slot_empty[slot]);
-    }
+  auto advance = [&] {
     if (++slot == kSlots) slot = 0, round ^= 1;
-    return true;
+  };
+  // S of key half h = Q K^T, K in slot `sl`
+  auto scores = [&](uint32_t sl, int h) {
+    tc_fence_after();
+    const uint64_t kd = k_desc + sl * kSlotLo + h * (kHalf * 128 >> 4);
+    if (leader) {
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * 128 * 128 + 32 * (kk & 3)) >> 4;
+        mma_bf16_ss(s_col + kHalf * h, q_desc + off, kd + off, id_qk, kk > 0 ? 1u : 0u);
+      }
+      mma_commit(&s.s_full[x][h]);
+    }
+  };
+  // an item's slot is free again once this tile's products that read it are done (at once where there are none)
+  auto release = [&](uint32_t sl, bool used) {
+    if (used && leader) mma_commit(&s.slot_empty[sl]);
+    if (!used && lane == 0) mbar_arrive(&s.slot_empty[sl]);
   };
   bool ok = true;
   while (ok && walk.next(sg)) {
@@ -224,39 +229,56 @@ __device__ void mma_issuer(Smem<D>& s, const AttnParams& p, const Share& sh, int
     const int n = sg.j1 - sg.j0, nx = steps_of(p, sg, x);
     ok = wait(&s.q_full, segs++, 0xA11);
     if (ok && nx == 0 && lane == 0) mbar_arrive(&s.q_empty);
-    ok = ok && key_item(nx > 0, nx == 1);
-    for (int j = 0; j < n && ok; ++j) {
-      ok = wait(&s.slot_full[slot], round, 0xA13);
-      if (ok && on_edge<kKeys>(p.window, p.sinks, u.pos0, u.pos0 + u.n - 1, u.held, tile_of(u, sg.j0 + j) * kKeys)) {
-        if (j < nx) ok = wait(&s.slot_fixed[slot], fixed >> slot, 0xA14);
+    ok = ok && wait(&s.slot_full[slot], round, 0xA12);
+    if (!ok) break;
+    if (nx > 0) {
+      scores(slot, 1);
+      scores(slot, 0);
+    }
+    release(slot, nx > 0);
+    if (nx == 1 && leader) mma_commit(&s.q_empty);
+    advance();
+    for (int j = 0; j < n; ++j) {
+      const bool use_v = j < nx, use_k = j + 1 < nx;
+      const uint32_t k_slot = slot;
+      if (j + 1 < n) {
+        if (!(ok = wait(&s.slot_full[slot], round, 0xA13))) break;
+        if (use_k) {  // the second half's scores are in registers: the next ones can take their place
+          if (!(ok = wait(&s.s_read[x], pc, 0xA18))) break;
+          scores(k_slot, 1);
+        }
+        advance();
+      }
+      if (!(ok = wait(&s.slot_full[slot], round, 0xA13))) break;
+      if (on_edge<kKeys>(p.window, p.sinks, u.pos0, u.pos0 + u.n - 1, u.held, tile_of(u, sg.j0 + j) * kKeys)) {
+        if (use_v && !(ok = wait(&s.slot_fixed[slot], fixed >> slot, 0xA14))) break;
         fixed ^= 1u << slot;
       }
-      if (ok && j == 0 && nx > 0 && oc > 0) ok = wait(&s.o_free[x], oc - 1, 0xA15);
-      if (!ok) break;
-      if (j < nx) {
+      if (use_v) {
+        if (j == 0 && oc > 0 && !(ok = wait(&s.o_free[x], oc - 1, 0xA15))) break;
         const uint64_t vd = v_desc + slot * kSlotLo;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 1; h >= 0; --h) {  // (P of keys 64 .. 127 comes first)
           if (ok) ok = wait(&s.p_full[x][h], pc, 0xA16);
           tc_fence_after();
           if (leader && ok) {
 #pragma unroll
             for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-              mma_bf16_ts(o_col, s_col + 8 * kk, vd + (2048 >> 4) * kk, id_pv, (j > 0 || kk > 0) ? 1u : 0u);
+              mma_bf16_ts(o_col, s_col + 8 * kk, vd + (2048 >> 4) * kk, id_pv, (j > 0 || kk != 4) ? 1u : 0u);
           }
         }
         if (!ok) break;
         ++pc;
-        if (leader) {
-          mma_commit(&s.slot_empty[slot]);
-          if (j == nx - 1) mma_commit(&s.o_full[x]);
+        if (!use_k) {
+          if (leader) mma_commit(&s.o_full[x]);
+          ++oc;
         }
-        oc += j == nx - 1;
-      } else if (lane == 0) {
-        mbar_arrive(&s.slot_empty[slot]);
       }
-      if (++slot == kSlots) slot = 0, round ^= 1;
-      if (j + 1 < n) ok = key_item(j + 1 < nx, j + 2 == nx);
+      release(slot, use_v);
+      if (use_k) scores(k_slot, 0);
+      if (j + 1 < n) release(k_slot, use_k);
+      if (j + 2 == nx && leader) mma_commit(&s.q_empty);
+      advance();
     }
   }
   if (!ok && lane == 0) fail(s, p, where);
@@ -282,11 +304,13 @@ __device__ void fixer(Smem<D>& s, const AttnParams& p, const Share& sh) {
     const int hi = min(last, u.held - 1), all = min(u.pos0, u.held - 1);  // up to `all`: no row is too early
     const int lo = p.window > 0 && u.pos0 >= p.window ? u.pos0 - p.window + 1 : 0;
     const int from = p.window > 0 && last >= p.window ? last - p.window + 1 : 0;  // from here on: no window is past
-    for (int j = sg.j0; j < sg.j1; ++j) {
-      const int key0 = tile_of(u, j) * kKeys;
-      for (int kv = 0; kv < 2; ++kv, ++item) {
+    for (int j = sg.j0 - 1; j < sg.j1; ++j) {
+      const int key0 = tile_of(u, max(j, sg.j0)) * kKeys;
+      for (int kv = 0; kv < 2; ++kv) {
+        if (kv == 0 ? j + 1 >= sg.j1 : j < sg.j0) continue;
         const int sl = item % kSlots;
         bool ok = mbar_wait_sleep(&s.slot_full[sl], (item / kSlots) & 1, &s.abort, 2 * p.wait_ns, 64);
+        ++item;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
           if (lane == 0) fail(s, p, 0xA21);
@@ -556,42 +580,41 @@ struct Steps {
   uint32_t sc;                   // key tiles of this tile so far
 };
 
-// Scores at Tensor Memory column 256 x, P in the columns of scores that have been read.
+// Scores of keys 64 h .. at Tensor Memory column 256 x + 64 h, all of P in the first half's columns.  The second half
+// is worked on first: its scores are computed while the previous step's P is still being made, so its exponentials run
+// during the products that the first half's scores wait for.  They use the reference as it stands; where the first half
+// then moves it, P of the second half is scaled (by a power of two, as references are whole numbers).
 template <int D>
 __device__ __noinline__ bool softmax_steps(Smem<D>& s, const Steps t, float& ref_out, float& l_out) {
   // (copies that no memory clobber makes the compiler read again)
   const int x = t.x, steps = t.n, last = t.last, sinks = t.sinks, ahead = t.ahead, lo_t = t.lo_t;
   const int win_lo = t.window > 0 && t.pos >= t.window ? t.pos - t.window + 1 : 0;  // the row's window
-  const int full_hi = min(t.first_pos, t.held - 1) - (kKeys - 1);                   // key tiles from here on: not every row sees all
-  const int past = t.window > 0 ? t.last_pos - t.window : -1;                       // key tiles up to here: neither ...
-  const int from = t.sinks - kKeys;                                                 // ... unless they come before that
+  const int full_hi = min(t.first_pos, t.held - 1) - (kHalf - 1);  // halves from here on: not every row sees all of them
+  const int past = t.window > 0 ? t.last_pos - t.window : -1;      // halves up to here: neither ...
+  const int from = t.sinks - kHalf;                                // ... unless they come before that
   const uint32_t sc = t.sc;
   const uint64_t wait_ns = t.wait_ns;
   const float a = t.a;
+  const float2 a2 = make_float2(a, a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t s_addr = s.tmem_base + ((uint32_t)(32 * (warp & 3)) << 16) + 256 * x;
-  uint64_t* const s_full = &s.s_full[x];
+  uint64_t* const s_full = s.s_full[x];
   uint64_t* const p_full = s.p_full[x];
   float ref = -INFINITY;  // row reference (base 2)
   float l = 0.f;          // row sum of 2^(x - ref)
   int tile = t.tile;
-#pragma unroll 1
-  for (int j = 0; j < steps; ++j) {
-    const int key0 = tile * kKeys;
-    tile = j + 1 == ahead ? lo_t : tile + 1;
-    const bool edge = (key0 > full_hi) | ((key0 <= past) & (key0 > from));
-    if (!warp_wait(s_full, sc + j, &s.abort, wait_ns)) return false;
-    tc_fence_after();
-    uint32_t r[4][32];
+  uint32_t r[2][32];
+  // the scores of 64 keys from k0 on, -infinity where this row does not see them; returns their maximum
+  auto load = [&](int h, int k0) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, r[c]);
+    for (int c = 0; c < 2; ++c) tmem_ld32(s_addr + kHalf * h + 32 * c, r[c]);
     tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld32_done(r[c]);
-    if (edge) {
-      const int hi = last + 1 - key0, lo = win_lo - key0, sk = sinks - key0;
+    for (int c = 0; c < 2; ++c) tmem_ld32_done(r[c]);
+    if ((k0 > full_hi) | ((k0 <= past) & (k0 > from))) {
+      const int hi = last + 1 - k0, lo = win_lo - k0, sk = sinks - k0;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         const uint32_t seen = below(hi - 32 * c) & (~below(lo - 32 * c) | below(sk - 32 * c));
 #pragma unroll
         for (int b = 0; b < 32; ++b) r[c][b] = (seen & (1u << b)) ? r[c][b] : 0xff800000u;
@@ -599,49 +622,80 @@ __device__ __noinline__ bool softmax_steps(Smem<D>& s, const Steps t, float& ref
     }
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int e = 0; e < 128; e += 8)
+    for (int e = 0; e < 64; e += 8)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         mx[c] = max3_nan(mx[c], __uint_as_float(r[e >> 5][(e & 31) + 2 * c]), __uint_as_float(r[e >> 5][(e & 31) + 2 * c + 1]));
-    const float mt = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * a;
-    // The reference moves to the row maximum at the first finite score and whenever a score passes it by more than 2^8.
-    // (S(j) is complete, so P(j - 1) V_{j-1} in front of it is too, and O may be changed.)
-    const bool need = ref == -INFINITY ? mt > -INFINITY : mt - ref > kRescale;
-    if (__any_sync(0xffffffffu, need)) {
-      const float f = !need ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx(ref - mt));
-      if (j > 0) rescale<D>(s_addr + 128, f);
-      if (need) ref = mt;
-      l *= f;
-    }
+    return max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * a;
+  };
+  // P of the scores at hand as bf16 pairs, and its sum
+  auto exponentials = [&](uint32_t (&pk)[32]) {
     const float neg = ref == -INFINITY ? 0.f : -ref;  // (a score of +infinity makes the row NaN)
-    const float2 a2 = make_float2(a, a), n2 = make_float2(neg, neg);
+    const float2 n2 = make_float2(neg, neg);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    uint32_t pk[64];
-    auto exponentials = [&](int e0, int e1) {
 #pragma unroll
-      for (int e = e0; e < e1; ++e) {
-        const float2 y = fma2(make_float2(__uint_as_float(r[e >> 4][(2 * e) & 31]), __uint_as_float(r[e >> 4][(2 * e + 1) & 31])),
-                              a2, n2);
-        const float2 z = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-        sum[e & 1] = add2(sum[e & 1], z);
-        pk[e] = pack2(z.x, z.y);
-      }
-    };
-    auto hand_over = [&](int h) {
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[h]);
-    };
-    exponentials(0, 32);
-    tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-    exponentials(32, kLate);  // (while the stores are under way)
-    hand_over(0);
-    exponentials(kLate, 64);
-    tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+    for (int e = 0; e < 32; ++e) {
+      const float2 y = fma2(make_float2(__uint_as_float(r[e >> 4][(2 * e) & 31]), __uint_as_float(r[e >> 4][(2 * e + 1) & 31])),
+                            a2, n2);
+      const float2 z = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+      sum[e & 1] = add2(sum[e & 1], z);
+      pk[e] = pack2(z.x, z.y);
+    }
     sum[0] = add2(sum[0], sum[1]);
     l += sum[0].x + sum[0].y;
-    hand_over(1);
+  };
+  // The reference moves to the row maximum (rounded up) at the first finite score and whenever a score passes it by more
+  // than 2^8; returns whether one of the warp's rows did, and what its sums have to be multiplied by.
+  auto move = [&](float mt, float& f) {
+    const bool need = ref == -INFINITY ? mt > -INFINITY : mt - ref > kRescale;
+    if (!__any_sync(0xffffffffu, need)) return false;
+    const float to = ceilf(mt);
+    f = !need ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx(ref - to));
+    if (need) ref = to;
+    l *= f;
+    return true;
+  };
+#pragma unroll 1
+  for (int j = 0; j < steps; ++j) {
+    const int key0 = tile * kKeys;
+    tile = j + 1 == ahead ? lo_t : tile + 1;
+    float f;
+    uint32_t ph[32], pl[32];
+    if (!warp_wait(&s_full[1], sc + j, &s.abort, wait_ns)) return false;
+    tc_fence_after();
+    const float mh = load(1, key0 + kHalf);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.s_read[x]);
+    if (move(mh, f) && j > 0) {
+      // (the first half's scores are computed behind the last product that adds to O)
+      if (!warp_wait(&s_full[0], sc + j, &s.abort, wait_ns)) return false;
+      tc_fence_after();
+      rescale<D>(s_addr + 128, f);
+    }
+    exponentials(ph);
+    if (!warp_wait(&s_full[0], sc + j, &s.abort, wait_ns)) return false;
+    tc_fence_after();
+    const float ml = load(0, key0);
+    if (move(ml, f)) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&ph[e]));
+        ph[e] = pack2(y.x * f, y.y * f);
+      }
+      if (j > 0) rescale<D>(s_addr + 128, f);
+    }
+    tmem_st32(s_addr + 32, ph);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&p_full[1]);
+    exponentials(pl);
+    tmem_st32(s_addr, pl);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&p_full[0]);
   }
   ref_out = ref;
   l_out = l;
@@ -806,8 +860,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.slot_fixed[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.s_full[i], 1);
-      for (int h = 0; h < 2; ++h) mbar_init(&s.p_full[i][h], 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&s.s_full[i][h], 1);
+        mbar_init(&s.p_full[i][h], 4);
+      }
+      mbar_init(&s.s_read[i], 4);
       mbar_init(&s.o_full[i], 1);
       mbar_init(&s.o_free[i], 4);
     }
