@@ -21,6 +21,7 @@
 // Every wait is bounded (MR_ERR_TIMEOUT, then drain and free Tensor Memory).
 #include <cuda_bf16.h>
 
+#include "attn_ptx.cuh"
 #include "attn_units.cuh"
 #include "kernels.h"
 #include "profile.h"
@@ -410,6 +411,7 @@ __device__ __noinline__ void rows_one_by_one(const AttnParams& p, const Seg& sg,
     const int tok = x * p.tile_tokens + r - hh * p.tile_tokens;
     if (hh >= sg.heads || tok >= u.n) continue;
     const int h = sg.h0 + hh, row = u.q0 + tok, pos = u.pos0 + tok;
+    if (!checked(p.ws, h < p.H_q && row < p.total_q, 0xC52)) continue;
     const __nv_bfloat16* q = (const __nv_bfloat16*)p.q + (int64_t)h * p.q_head + (int64_t)row * p.q_row + C * lane;
     float qf[C], acc[C];
 #pragma unroll
@@ -578,6 +580,7 @@ struct Steps {
   int held, pos, last;           // rows the table covers; this row's position, the last row it sees
   int tile, ahead, lo_t;         // first key tile; after `ahead` of them the list goes on at tile lo_t
   uint32_t sc;                   // key tiles of this tile so far
+  int skip;                      // failure-path test: the first P is not handed over
 };
 
 // Scores of keys 64 h .. at Tensor Memory column 256 x + 64 h, all of P in the first half's columns.  The second half
@@ -594,6 +597,7 @@ __device__ __noinline__ bool softmax_steps(Smem<D>& s, const Steps t, float& ref
   const int from = t.sinks - kHalf;                                // ... unless they come before that
   const uint32_t sc = t.sc;
   const uint64_t wait_ns = t.wait_ns;
+  const bool skip = t.skip != 0;
   const float a = t.a;
   const float2 a2 = make_float2(a, a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -689,7 +693,7 @@ __device__ __noinline__ bool softmax_steps(Smem<D>& s, const Steps t, float& ref
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&p_full[1]);
+    if (lane == 0 && !(skip && j == 0)) mbar_arrive(&p_full[1]);
     exponentials(pl);
     tmem_st32(s_addr, pl);
     tmem_wait_st();
@@ -727,7 +731,8 @@ __device__ void softmax_group(Smem<D>& s, const AttnParams& p, const Share& sh, 
     const int nx = steps_of(p, sg, x);
     float ref = -INFINITY, l = 0.f;
     if (nx > 0 && !softmax_steps<D>(s, Steps{p.a, wait_ns, p.window, p.sinks, x, nx, first_pos, last_pos, u.held, pos, last,
-                                   tile_of(u, sg.j0), u.ns - sg.j0, u.lo_t, sc},
+                                   tile_of(u, sg.j0), u.ns - sg.j0, u.lo_t, sc,
+                                   p.skip_arrive && x == 0 && sc == 0},
                           ref, l))
       return fail(s, p, 0xA31);
     sc += nx;
@@ -743,6 +748,7 @@ __device__ void softmax_group(Smem<D>& s, const AttnParams& p, const Share& sh, 
     float* slot = nullptr;
     if (!whole) {
       holders(sh, sg, first, lastc);
+      if (!checked(p.ws, first >= 0 && lastc < kMaxCtas && (int)blockIdx.x <= lastc, 0xC53)) return fail(s, p, 0xC53);
       slot = slot_ptr<D>(p, slot_of(blockIdx.x, first));
     }
     if (slow) {
@@ -767,6 +773,7 @@ __device__ void softmax_group(Smem<D>& s, const AttnParams& p, const Share& sh, 
         for (int e = 0; e < D; ++e) o[e >> 5][e & 31] = 0;
       }
       if (row_ok && whole) {
+        if (!checked(p.ws, h < p.H_q && row < p.total_q, 0xC51)) continue;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (p.lse) p.lse[(int64_t)h * p.total_q + row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
         __nv_bfloat16* out = (__nv_bfloat16*)p.o + (int64_t)h * p.o_head + (int64_t)row * p.o_row;
@@ -947,7 +954,8 @@ bool launch_attn_tc(const AttnArgs& a, AttnParams p, int sms, cudaError_t* resul
   p.negate = p.a < 0.f;
   p.a = p.a == 0.f ? 1e-30f : fabsf(p.a);
   if (((uintptr_t)a.o.ptr | (uintptr_t)(a.o.head_stride * 2) | (uintptr_t)(a.o.row_stride * 2)) % 32 == 0) p.vec_o = 2;
-  p.wait_ns = kTimeoutNs;
+  debug_waits(&p.wait_ns, &p.skip_arrive);
+  if (p.wait_ns == 0) p.wait_ns = kTimeoutNs;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   *result = d == 64 ? launch<64>(maps, p, box, grid, a.stream) : launch<128>(maps, p, box, grid, a.stream);
   return true;

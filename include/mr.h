@@ -662,7 +662,8 @@ mr_status mr_gather_probe(const mr_bsr* map, int readers, int ring_slots, void* 
  * skip_arrive = 1, makes the softmax warpgroup of each CTA's first query tile withhold its first
  * "P ready" arrive, so the MMA warp's wait runs out: the call records MR_ERR_TIMEOUT (detail
  * 0x913) in the workspace's status word, drains its copies and MMAs, frees Tensor Memory and
- * returns, leaving the context usable.
+ * returns, leaving the context usable.  mr_paged_attn's tensor-core kernel obeys the same two settings
+ * (detail 0xA16).
  * mr_debug_set(0, 0) restores normal operation.  No GPU fault is involved.
  */
 mr_status mr_debug_set(uint64_t wait_ns, int skip_arrive);
