@@ -586,7 +586,7 @@ struct Steps {
 // Scores of keys 64 h .. at Tensor Memory column 256 x + 64 h, all of P in the first half's columns.  The second half
 // is worked on first: its scores are computed while the previous step's P is still being made, so its exponentials run
 // during the products that the first half's scores wait for.  They use the reference as it stands; where the first half
-// then moves it, P of the second half is scaled (by a power of two, as references are whole numbers).
+// then moves it (in a segment's first steps, hardly later), P of the second half is scaled, at most 2^-8, and rounded again.
 template <int D>
 __device__ __noinline__ bool softmax_steps(Smem<D>& s, const Steps t, float& ref_out, float& l_out) {
   // (copies that no memory clobber makes the compiler read again)
@@ -648,14 +648,13 @@ __device__ __noinline__ bool softmax_steps(Smem<D>& s, const Steps t, float& ref
     sum[0] = add2(sum[0], sum[1]);
     l += sum[0].x + sum[0].y;
   };
-  // The reference moves to the row maximum (rounded up) at the first finite score and whenever a score passes it by more
-  // than 2^8; returns whether one of the warp's rows did, and what its sums have to be multiplied by.
+  // The reference moves to the row maximum at the first finite score (so a row that sees one key gives it exactly 1) and
+  // whenever a score passes it by more than 2^8; returns whether one of the warp's rows did, and what its sums have to be multiplied by.
   auto move = [&](float mt, float& f) {
     const bool need = ref == -INFINITY ? mt > -INFINITY : mt - ref > kRescale;
     if (!__any_sync(0xffffffffu, need)) return false;
-    const float to = ceilf(mt);
-    f = !need ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx(ref - to));
-    if (need) ref = to;
+    f = !need ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx(ref - mt));
+    if (need) ref = mt;
     l *= f;
     return true;
   };

@@ -384,6 +384,20 @@ def test_attn_on_a_stream_and_in_a_graph(mr, dt):
         assert torch.equal(out, mr.paged_attn(cache, table, lens, q, c.cu))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_that_see_one_key_give_its_value(mr, dt):
+    """softmax of one score is 1: nothing is left to round."""
+    c = Case(mr, [90, 1], [130, 1], 8, 2, 16, 128, dt, seed=14)
+    cache, table, lens, q = c.args()
+    O, lse = mr.paged_attn(cache, table, lens, q, c.cu, window=1, return_lse=True, ws=c.ws)
+    pos = np.concatenate([np.arange(40, 130), [0]])
+    seq = np.array([0] * 90 + [1])
+    v = c.v[c.table[seq, pos // 16].long(), :, pos % 16].transpose(0, 1).repeat_interleave(4, 0)
+    assert torch.equal(O, v)
+    one = mr.paged_decode(cache, table, lens, q[:, :2].contiguous(), window=1, ws=c.ws)
+    assert torch.equal(one, v[:, [89, 90]])
+
+
 # ---------------------------------------------------------------------------------------------- streams that are given
 @pytest.mark.parametrize("handle", [False, True])
 def test_a_given_stream_without_a_workspace(mr, handle):
