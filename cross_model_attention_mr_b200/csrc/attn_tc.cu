@@ -14,8 +14,8 @@
 //   * two softmax warpgroups, a query row per thread: the mask only where some row does not see some key, a row reference
 //     that moves when a score passes it by 2^8 (O is then rescaled in Tensor Memory), P = 2^(x - reference) in bf16;
 //   * a fix-up warp looks after the values of key tiles that not every row sees: rows that nobody of the unit sees become
-//     zeros (0 * NaN would not be 0); rows that only some see are searched for values that are not finite, and where
-//     there are any the segment's rows are computed again one by one.
+//     zeros (0 * NaN would not be 0); in rows that only some see, values that are not finite do, and the softmax warps
+//     add them at the end to the rows that do see them.
 // Bound by the exponentials (16384 per tile at 16 a clock take as long as the tile's two products) and by the chain
 // S -> softmax -> P V -> S of each tile.
 // Every wait is bounded (MR_ERR_TIMEOUT, then drain and free Tensor Memory).
@@ -69,7 +69,7 @@ struct Smem {
   PartitionSmem part;
   uint32_t tmem_base;
   int abort;
-  int slow[kSlowRing];  // segment number + 1 where the rows have to be computed one by one
+  int slow[kSlowRing];  // segment number + 1 where values were taken out
   int join;
 };
 
@@ -97,6 +97,12 @@ __device__ __forceinline__ bool on_edge(int window, int sinks, int first, int la
 
 // Bits 0 .. n - 1, for any n.
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u; }
+
+// Mask of the bf16 halves of w that are infinite or NaN (an exponent of all ones carries into the bit above when one is
+// added to it).
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  return ((((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) >> 15) * 0xffffu;
+}
 
 // Key tiles of the segment that tile x of the unit needs (a front part of them), 0 for a missing tile.
 __device__ __forceinline__ int steps_of(const AttnParams& p, const Seg& sg, int x) {
@@ -341,14 +347,18 @@ __device__ void fixer(Smem<D>& s, const AttnParams& p, const Share& sh) {
                 for (int c = 0; c < kHalves; ++c)
                   y[g][c] = *reinterpret_cast<const uint4*>(v + c * 128 * 128 + (g0 + g) * 512);
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                uint32_t hit = 0;  // (an exponent of all ones carries into bit 15 or 31 when one is added to it)
+              for (int g = 0; g < 4; ++g)
 #pragma unroll
-                for (int c = 0; c < kHalves; ++c)
-                  hit |= ((y[g][c].x & 0x7f807f80u) + 0x00800080u) | ((y[g][c].y & 0x7f807f80u) + 0x00800080u) |
-                         ((y[g][c].z & 0x7f807f80u) + 0x00800080u) | ((y[g][c].w & 0x7f807f80u) + 0x00800080u);
-                bad |= (look >> g & 1u) ? hit & 0x80008000u : 0u;
-              }
+                for (int c = 0; c < kHalves; ++c) {
+                  const uint32_t hit = (look >> g & 1u) ? not_finite(y[g][c].x) | not_finite(y[g][c].y) |
+                                                              not_finite(y[g][c].z) | not_finite(y[g][c].w)
+                                                        : 0u;
+                  bad |= hit;
+                  if (hit)
+                    *reinterpret_cast<uint4*>(v + c * 128 * 128 + (g0 + g) * 512) =
+                        make_uint4(y[g][c].x & ~not_finite(y[g][c].x), y[g][c].y & ~not_finite(y[g][c].y),
+                                   y[g][c].z & ~not_finite(y[g][c].z), y[g][c].w & ~not_finite(y[g][c].w));
+                }
             }
             if (__any_sync(0xffffffffu, dead != 0)) {
 #pragma unroll
@@ -399,67 +409,51 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t (&q)[8], bool 
   }
 }
 
-// 32 rows of a tile one by one (a lane per D / 32 columns): where values that are not finite would reach rows that
-// do not see them.
+// Adds what the fix-up warp has taken out: p_j v_j for the elements of v_j that are not finite, where this lane's row
+// sees key j.  The warp looks through the values of the segment's tiles that not every row sees; O is in Tensor Memory.
 template <int D>
-__device__ __noinline__ void rows_one_by_one(const AttnParams& p, const Seg& sg, int x, int row0, bool whole, float* slot) {
+__device__ __noinline__ void put_back(const AttnParams& p, const Seg& sg, uint32_t o_addr, int pos, int last, float ref,
+                                      const __nv_bfloat16* q) {
   constexpr int C = D / 32;
   const int lane = threadIdx.x & 31;
   const Unit& u = sg.u;
-  for (int r = row0; r < row0 + 32; ++r) {
-    const int hh = (int)fast_div((uint32_t)r, p.by_tile_tokens);
-    const int tok = x * p.tile_tokens + r - hh * p.tile_tokens;
-    if (hh >= sg.heads || tok >= u.n) continue;
-    const int h = sg.h0 + hh, row = u.q0 + tok, pos = u.pos0 + tok;
-    if (!checked(p.ws, h < p.H_q && row < p.total_q, 0xC52)) continue;
-    const __nv_bfloat16* q = (const __nv_bfloat16*)p.q + (int64_t)h * p.q_head + (int64_t)row * p.q_row + C * lane;
-    float qf[C], acc[C];
+  const int u_last = u.pos0 + u.n - 1, hi = min(u_last, u.held - 1);
+  const int lo = p.window > 0 && u.pos0 >= p.window ? u.pos0 - p.window + 1 : 0;
+  const float a = p.negate ? -p.a : p.a;
+  for (int j = sg.j0; j < sg.j1; ++j) {
+    const int key0 = tile_of(u, j) * kKeys;
+    if (!on_edge<kKeys>(p.window, p.sinks, u.pos0, u_last, u.held, key0)) continue;
+    for (int key = key0; key < key0 + kKeys && key <= hi; ++key) {
+      if (key < lo && key >= p.sinks) continue;
+      const int at = pool_row(p.kv, u.s, sg.g, key);
+      if (at < 0) continue;
+      const __nv_bfloat16* v = (const __nv_bfloat16*)p.kv.v + (int64_t)at * D;
+      uint32_t bad = 0;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      qf[c] = __bfloat162float(q[c]);
-      acc[c] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int j = sg.j0; j < sg.j1; ++j) {
-      const int key0 = tile_of(u, j) * kKeys;
-      for (int key = key0; key < key0 + kKeys; ++key) {
-        if (key > min(pos, u.held - 1) || (p.window > 0 && key <= pos - p.window && key >= p.sinks)) continue;
-        const int at = pool_row(p.kv, u.s, sg.g, key);
-        float kf[C], vf[C], sc = 0.f;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const int64_t e = (int64_t)max(at, 0) * D + C * lane + c;
-          kf[c] = at < 0 ? 0.f : __bfloat162float(((const __nv_bfloat16*)p.kv.k)[e]);
-          vf[c] = at < 0 ? 0.f : __bfloat162float(((const __nv_bfloat16*)p.kv.v)[e]);
-          sc = fmaf(qf[c], kf[c], sc);
-        }
-#pragma unroll
-        for (int w = 16; w; w >>= 1) sc += __shfl_xor_sync(0xffffffffu, sc, w);
-        sc *= p.a;
-        float f = 1.f;
-        if (sc > m) {
-          f = ex2_approx(m - sc);
-          m = sc;
-        }
-        const float e = ex2_approx(sc - (m == -INFINITY ? 0.f : m));
-        l = fmaf(l, f, e);
-#pragma unroll
-        for (int c = 0; c < C; ++c) acc[c] = fmaf(acc[c], f, e * vf[c]);
+      for (int c = 0; c < C; c += 2) bad |= not_finite(*reinterpret_cast<const uint32_t*>(v + C * lane + c));
+      if (!__any_sync(0xffffffffu, bad != 0)) continue;
+      const bool sees = key <= last && (p.window == 0 || pos < p.window || key > pos - p.window || key < p.sinks);
+      float e = 0.f;
+      if (sees) {
+        const __nv_bfloat16* k = (const __nv_bfloat16*)p.kv.k + (int64_t)at * D;
+        float x = 0.f;
+        for (int c = 0; c < D; ++c) x = fmaf(__bfloat162float(q[c]), __bfloat162float(k[c]), x);
+        e = ex2_approx(fmaf(x, a, ref == -INFINITY ? 0.f : -ref));
       }
-    }
-    if (whole) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      __nv_bfloat16* o = (__nv_bfloat16*)p.o + (int64_t)h * p.o_head + (int64_t)row * p.o_row + C * lane;
+      __syncwarp();
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_addr + c, o);
+        tmem_wait_ld();
+        tmem_ld32_done(o);
 #pragma unroll
-      for (int c = 0; c < C; ++c) o[c] = __float2bfloat16_rn(acc[c] * inv);
-      if (lane == 0 && p.lse) p.lse[(int64_t)h * p.total_q + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    } else {
-      const int at = 128 * x + r;
-      if (lane == 0) __stcg(reinterpret_cast<float2*>(slot) + at, make_float2(m, l));
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int col = C * lane + c;
-        __stcg(reinterpret_cast<float*>(slot_out<D>(slot, col >> 2, at)) + (col & 3), acc[c]);
+        for (int t = 0; t < 32; ++t) {
+          const float y = __bfloat162float(v[c + t]);
+          if (sees && !isfinite(y)) o[t] = __float_as_uint(fmaf(e, y, __uint_as_float(o[t])));
+        }
+        tmem_st32(o_addr + c, o);
+        tmem_wait_st();
       }
     }
   }
@@ -750,12 +744,11 @@ __device__ void softmax_group(Smem<D>& s, const AttnParams& p, const Share& sh, 
       if (!checked(p.ws, first >= 0 && lastc < kMaxCtas && (int)blockIdx.x <= lastc, 0xC53)) return fail(s, p, 0xC53);
       slot = slot_ptr<D>(p, slot_of(blockIdx.x, first));
     }
-    if (slow) {
-      rows_one_by_one<D>(p, sg, x, 32 * q4, whole, slot);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.o_free[x]);
-    } else {
+    if (slow)
+      put_back<D>(p, sg, o_addr, pos, last, ref,
+                  (const __nv_bfloat16*)p.q + (int64_t)(row_ok ? h : sg.h0) * p.q_head +
+                      (int64_t)(row_ok ? row : u.q0) * p.q_row);
+    {
       uint32_t o[D / 32][32];
       __syncwarp();
       if (nx > 0) {

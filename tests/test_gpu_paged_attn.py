@@ -303,6 +303,26 @@ def test_attn_rows_that_only_some_see(mr, dt, what, bad):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.2, -0.2])
+def test_attn_values_that_only_some_see_in_split_units(mr, dt, scale):
+    """The same where many CTAs share a unit, with either sign of the scale: what is finite stays right, rows that see the
+    infinite value get it (its own weight's sign), the others do not."""
+    c = Case(mr, [64], [5000], 2, 1, 16, 128, dt, seed=15)
+    cache, table, lens, q = c.args()
+    want, wl = mr.paged_attn(cache, table, lens, q, c.cu, scale=scale, return_lse=True, ws=c.ws)
+    c.check(want, wl, scale=scale, p_eps=ATTN_P[dt])
+    for row, col in ((4990, 3), (4950, 127), (4999, 64)):
+        c.v[c.table[0, row // 16], 0, row % 16, col] = math.inf
+    got, gl = mr.paged_attn(cache, table, lens, q, c.cu, scale=scale, return_lse=True, ws=c.ws)
+    assert torch.equal(gl, wl)
+    for row, col in ((4990, 3), (4950, 127), (4999, 64)):
+        i = row - 4936                                     # the first new row that sees it
+        assert bool((got[:, i:, col] == math.inf).all()) and bool(torch.isfinite(got[:, :i, col]).all())
+        got[:, i:, col] = want[:, i:, col]
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_attn_strides_and_alignment(mr, dt):
     c = Case(mr, [40, 3], [50, 120], 6, 2, 16, 64, dt, seed=8)
     cache, table, lens, q = c.args()
@@ -396,6 +416,30 @@ def test_rows_that_see_one_key_give_its_value(mr, dt):
     assert torch.equal(O, v)
     one = mr.paged_decode(cache, table, lens, q[:, :2].contiguous(), window=1, ws=c.ws)
     assert torch.equal(one, v[:, [89, 90]])
+
+
+# ---------------------------------------------------------------------------------------------- pools beyond 2^32 bytes
+def test_pages_far_into_a_large_pool(mr):
+    """Rows whose byte offsets pass 32 bits (a pool of 5.2 GB for keys and one for values): appended, read and copied."""
+    n_pages, pr, d = 160000, 128, 128
+    cache = mr.KVCache.empty(n_pages, 1, pr, d)
+    table = torch.tensor([[n_pages - 1, 5, n_pages - 3], [131073, n_pages - 7, 131072]], dtype=torch.int32).cuda()
+    lens = torch.tensor([300, 257], dtype=torch.int32).cuda()
+    cu = torch.tensor([0, 300, 557], dtype=torch.int32).cuda()
+    q, k, v = rand((4, 557, d), "bf16", 1), rand((1, 557, d), "bf16", 2), rand((1, 557, d), "bf16", 3)
+    ws = mr.Workspace(mr.paged_workspace_bytes(cache, 4, 2))
+    mr.kv_append(cache, table, lens, k, v, cu_q=cu, ws=ws)
+    assert ws.sync_status() == mr.MR_OK
+    small = mr.KVCache.empty(6, 1, pr, d)
+    near = torch.arange(6, dtype=torch.int32).view(2, 3).cuda()
+    mr.kv_append(small, near, lens, k, v, cu_q=cu, ws=ws)
+    assert torch.equal(cache.k[table.view(-1)[:2].long()], small.k[:2])
+    want = mr.paged_attn(small, near, lens, q, cu, ws=ws)
+    assert torch.equal(mr.paged_attn(cache, table, lens, q, cu, ws=ws), want) and ws.sync_status() == mr.MR_OK
+    one = q[:, [299, 556]].contiguous()
+    assert torch.equal(mr.paged_decode(cache, table, lens, one), mr.paged_decode(small, near, lens, one))
+    mr.pages_copy([cache.k, cache.v], torch.tensor([[n_pages - 1, 140000]], dtype=torch.int32).cuda(), ws=ws)
+    assert torch.equal(cache.v[140000], small.v[0]) and ws.sync_status() == mr.MR_OK
 
 
 # ---------------------------------------------------------------------------------------------- streams that are given
