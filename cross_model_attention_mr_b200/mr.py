@@ -645,6 +645,11 @@ def _rows(t: torch.Tensor, like: torch.Tensor, what: str) -> Rows:
     return Rows(t.data_ptr(), stride[0], stride[1])
 
 
+def _new_like(t: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _ints(t: torch.Tensor, like: torch.Tensor, what: str, dim: int = 1) -> int:
     """Address of a contiguous int32 tensor on the device of `like`."""
     if t.dtype is not torch.int32 or t.dim() != dim or not t.is_contiguous():
@@ -692,7 +697,7 @@ def rope(r: Rope, X: torch.Tensor, pos: torch.Tensor, out: Optional[torch.Tensor
         if pos.shape[0] != n:
             raise ValueError("pos must give one position per row")
         if out is None:
-            out = torch.empty((H, n, d), dtype=X.dtype, device=X.device)
+            out = _new_like(X)
         elif out.shape != X.shape:
             raise ValueError("out must have the shape of X")
         check(LIB.mr_rope_apply(ctypes.byref(r.c), ctypes.byref(x), ctypes.byref(_rows(out, X, "out")), dt, H, n,
@@ -758,7 +763,7 @@ def kv_append(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, K: torc
             if Q.shape[1:] != K.shape[1:]:
                 raise ValueError("Q must be [H_q][total_q][d]")
             if q_out is None:
-                q_out = torch.empty((H_q, total, cache.d), dtype=Q.dtype, device=Q.device)
+                q_out = _new_like(Q)
             elif q_out.shape != Q.shape:
                 raise ValueError("q_out must have the shape of Q")
             q, qo = ctypes.byref(_rows(Q, cache.k, "Q")), ctypes.byref(_rows(q_out, cache.k, "q_out"))
@@ -777,9 +782,9 @@ def kv_append(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, K: torc
 
 def _attn_out(Q: torch.Tensor, out, lse, return_lse: bool):
     """Output and log-normaliser tensors of an attention call on Q [H_q][rows][d]."""
-    H, n, d = Q.shape
+    H, n, _ = Q.shape
     if out is None:
-        out = torch.empty((H, n, d), dtype=Q.dtype, device=Q.device)
+        out = _new_like(Q)
     elif out.shape != Q.shape:
         raise ValueError("out must have the shape of Q")
     if lse is not None:
@@ -844,6 +849,8 @@ def pages_copy_workspace_bytes() -> int:
 def pages_copy(pools, pairs: torch.Tensor, ws: Optional[Workspace] = None, stream=None) -> None:
     """mr_pages_copy: page pairs[t][1] <- page pairs[t][0] (int32, device) in every pool (tensors
     [n_pages][...], e.g. the k and v of every layer's cache)."""
+    if not pools:
+        raise ValueError("no pools")
     first = pools[0]
     with _on(first, stream):
         page_bytes = first.stride(0) * first.element_size()

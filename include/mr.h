@@ -505,7 +505,9 @@ mr_status mr_rope_apply(const mr_rope* rope, const mr_rows* X, const mr_rows* Y,
                         int n_rows, const int32_t* pos, int adjoint, void* stream);
 
 /* Workspace bytes of mr_kv_append, mr_paged_decode and mr_paged_attn for a cache, H_q query heads and
- * n_seq sequences (device memory, 256-byte aligned).  0 for an unsupported shape. */
+ * n_seq sequences (device memory, 256-byte aligned).  0 for an unsupported shape.  The contents need
+ * not be set before a call nor kept after it, but for the status word; calls that can be under way at
+ * the same time (on other streams, or in graphs replayed side by side) need a workspace each. */
 size_t mr_paged_workspace_bytes(const mr_kv_cache* cache, int H_q, int n_seq);
 
 /*
