@@ -18,6 +18,8 @@
 // second product's operand as they are.  Probabilities are split into two bf16 parts (value and remainder)
 // so that their rounding does not show beside the output's own; with up to 8 heads both parts share one
 // instruction (rows 0-7 and 8-15).  fp32 runs on the CUDA cores.
+// 8 sequences of 32768 rows, 64 heads in groups of 8 (1.07 GB): 173 us, 6.2 TB/s, 94% of a copy's rate; 16 sequences of
+// 4608 to 6144 rows, 32 heads in groups of 4: 63 us, 5.6 TB/s.
 #include <cuda_bf16.h>
 
 #include "paged.cuh"

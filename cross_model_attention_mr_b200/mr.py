@@ -772,7 +772,7 @@ def kv_append(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, K: torc
         seqs = _seqs(cache, table, kv_len)
         if cu_q is not None and cu_q.shape[0] != seqs.n_seq + 1:
             raise ValueError("cu_q must have n_seq + 1 entries")
-        ws = _ws_for(ws, lambda: paged_workspace_bytes(cache, cache.H_kv, seqs.n_seq), cache.k)
+        ws = _ws_for(ws, lambda: 0, cache.k)  # (the status word is all this call needs)
         check(LIB.mr_kv_append(ctypes.byref(cache.c), ctypes.byref(seqs), ctypes.byref(rope.c) if rope else None, q, qo,
                                H_q, ctypes.byref(k), ctypes.byref(v),
                                _ints(cu_q, cache.k, "cu_q") if cu_q is not None else None, total, ws.ptr, ws.nbytes,

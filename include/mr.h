@@ -519,6 +519,7 @@ size_t mr_paged_workspace_bytes(const mr_kv_cache* cache, int H_q, int n_seq);
  *          NULL when every sequence has one new row (total_q == n_seq)
  *   total_q  host int, at least cu_q[n_seq]; rows at or behind cu_q[n_seq] are neither read nor
  *          written (their Q_out rows stay as they were)
+ * Of the workspace only the first 256 bytes are used.
  * A new row whose position is negative (kv_len[s] below its new rows) is not stored, its Q_out row is
  * zero.  Sequences that share a page (after a fork) must not append into it: copy it first.
  */

@@ -179,6 +179,19 @@ def test_pages_copy_refuses(mr):
     assert call(n_pages=2 ** 31) == mr.MR_ERR_UNSUPPORTED
 
 
+def test_python_refuses_what_is_not_on_a_gpu(mr):
+    import torch
+    x, pos = torch.zeros(2, 3, 64), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        mr.rope(mr.Rope(64), x, pos)
+    with pytest.raises(ValueError):
+        mr.KVCache(x[None], x[None])
+    with pytest.raises(ValueError):
+        mr.pages_copy([], pos.view(-1, 1))
+    with pytest.raises(ValueError):
+        mr.pages_copy([x], pos.view(-1, 1))
+
+
 # ------------------------------------------------------------------------------------------------ page pool
 def test_pool_extend_fork_and_copy_on_write(mr):
     pp = mr.PagePool(8, 16)
