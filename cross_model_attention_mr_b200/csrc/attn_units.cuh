@@ -97,7 +97,7 @@ struct Share {
 };
 
 struct PartitionSmem {
-  int64_t sums[32];
+  int64_t sums[32], all[32];
   int most[32];
   int64_t before;
   int s, r;
@@ -124,14 +124,28 @@ __device__ bool make_share(const AttnParams& p, PartitionSmem& sm, Share& sh) {
     }
     return w.s < n_seq;
   };
-  int64_t sum = 0;
-  int most = 0;
+  auto cost_at = [&](Walk& w, int64_t i) {
+    return advance(w, i) ? cost_of(p, make_unit<KT>(p, w.s, (int)(i - w.base), w.q0, w.n)) : 0;
+  };
+  // inclusive sum over the warp
+  auto scan = [&](int64_t x) {
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    return x;
+  };
+  // the first NT runs are added up in order (often there are no more), the others only as a total
+  Walk w;
+  int cost = cost_at(w, tid), most = cost;
+  int64_t upto = scan(cost), sum = cost;
   {
-    Walk w;
-    for (int64_t i = tid; advance(w, i); i += NT) {
-      const int cost = cost_of(p, make_unit<KT>(p, w.s, (int)(i - w.base), w.q0, w.n));
-      sum += cost;
-      most = max(most, cost);
+    Walk rest = w;
+    for (int64_t i = (int64_t)tid + NT; advance(rest, i); i += NT) {
+      const int c = cost_at(rest, i);
+      sum += c;
+      most = max(most, c);
     }
   }
 #pragma unroll
@@ -139,15 +153,16 @@ __device__ bool make_share(const AttnParams& p, PartitionSmem& sm, Share& sh) {
     sum += __shfl_xor_sync(0xffffffffu, sum, d);
     most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
   }
-  if (lane == 0) {
-    sm.sums[warp] = sum;
+  if (lane == 31) {
+    sm.sums[warp] = upto;
+    sm.all[warp] = sum;
     sm.most[warp] = most;
   }
   __syncthreads();
   int64_t steps = 0;
 #pragma unroll
   for (int i = 0; i < NT / 32; ++i) {
-    steps += sm.sums[i];
+    steps += sm.all[i];
     most = max(most, sm.most[i]);
   }
   const int64_t HC = (int64_t)p.kv.H_kv * p.chunks;
@@ -158,20 +173,15 @@ __device__ bool make_share(const AttnParams& p, PartitionSmem& sm, Share& sh) {
   if (k >= sh.ctas) return false;
   sh.cur = k * sh.total / sh.ctas;
   sh.end = (k + 1) * sh.total / sh.ctas;
-  Walk w;
-  int64_t front = 0;  // steps per head in front of the NT runs looked at
+  int64_t front = 0;  // steps per head in front of the NT runs at hand
   for (int64_t i = tid;; i += NT) {
-    const bool live = advance(w, i);
-    const int cost = live ? cost_of(p, make_unit<KT>(p, w.s, (int)(i - w.base), w.q0, w.n)) : 0;
-    int64_t upto = cost;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += y;
+    if (i != tid) {
+      cost = cost_at(w, i);
+      upto = scan(cost);
+      __syncthreads();
+      if (lane == 31) sm.sums[warp] = upto;
+      __syncthreads();
     }
-    __syncthreads();
-    if (lane == 31) sm.sums[warp] = upto;
-    __syncthreads();
     int64_t all = 0;
     upto += front;
 #pragma unroll
@@ -179,7 +189,7 @@ __device__ bool make_share(const AttnParams& p, PartitionSmem& sm, Share& sh) {
       if (v < warp) upto += sm.sums[v];
       all += sm.sums[v];
     }
-    if (live && sh.cur >= (upto - cost) * HC && sh.cur < upto * HC) {
+    if (cost > 0 && sh.cur >= (upto - cost) * HC && sh.cur < upto * HC) {
       sm.s = w.s;
       sm.r = (int)(i - w.base);
       sm.before = upto - cost;

@@ -271,6 +271,34 @@ def test_attn_many_units_and_parts(mr, dt, d):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_attn_many_sequences(mr, dt):
+    """More runs of new rows than a CTA has threads, some without rows, some that hold nothing."""
+    rng = np.random.default_rng(2)
+    new = rng.integers(0, 3, 1300)
+    held = np.maximum(new + rng.integers(-1, 40, 1300), 0)
+    new[:5], held[700:705] = 0, 0
+    c = Case(mr, new.tolist(), held.tolist(), 2, 1, 16, 64, dt, seed=16)
+    O, lse = mr.paged_attn(*c.args(), c.cu, window=20, sinks=2, return_lse=True, ws=c.ws)
+    c.check(O, lse, window=20, sinks=2, p_eps=ATTN_P[dt])
+
+
+def test_two_calls_at_once(mr):
+    """Two streams, a workspace each."""
+    a = Case(mr, [200, 1500], [700, 1500], 8, 2, 16, 128, "bf16", seed=17)
+    b = Case(mr, [1] * 6, [9000, 1, 300, 4000, 64, 20], 8, 2, 64, 128, "bf16", seed=18)
+    x, y = a.args(), b.args()
+    wa, wb = mr.paged_attn(*x, a.cu, window=400, ws=a.ws), mr.paged_decode(*y, ws=b.ws)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        got.append((mr.paged_attn(*x, a.cu, window=400, ws=a.ws, stream=s), mr.paged_decode(*y, ws=b.ws, stream=t)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, wa) and torch.equal(h, wb) for g, h in got)
+    assert a.ws.sync_status() == mr.MR_OK and b.ws.sync_status() == mr.MR_OK
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("what", ["k", "v"])
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 def test_attn_rows_that_only_some_see(mr, dt, what, bad):
