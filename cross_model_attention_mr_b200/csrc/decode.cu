@@ -4,7 +4,7 @@
 // 2 G operations a byte for groups of G heads, far below what the tensor cores do per byte read.  So the
 // design is about keeping loads in flight and every SM equally busy:
 //   * The visible rows of a sequence (first rows kept and the window) are numbered without the gap
-//     between them and cut into tiles of 64.  The tiles of all (sequence, kv head, chunk of up to 16 query
+//     between them and cut into tiles of 64.  The tiles of all (query row, kv head, chunk of up to 16 query
 //     heads) units, one unit after the other, are split evenly over the CTAs, which need not begin or end
 //     with a unit: ragged batches and single long sequences load the GPU alike.
 //   * A CTA that holds a whole unit writes its output; the parts of a unit that several CTAs share go to the
@@ -47,6 +47,8 @@ struct Params {
   void* o;
   int64_t q_head, q_row, o_head, o_row;  // strides in elements
   float* lse;
+  const int32_t* cu;                     // NULL: row t is sequence t's
+  int n_rows;
   int H_q, group, chunks, rows;          // chunks of `rows` query heads per kv head (the last may be shorter)
   int vec_q, vec_o;                      // rows aligned to 4 (Q) and 16 (O) bytes
   float a;                               // scale * log2(e)
@@ -111,20 +113,32 @@ __device__ __forceinline__ uint32_t pack2_rest(float x, float y, uint32_t hi) {
   return pack2(x - h.x, y - h.y);
 }
 
-// The visible rows of a sequence whose newest row is its query: rows [0, first) and [lo, lo + n - first).
+// Query row t: its sequence (-1: none, the row is left alone) and how many cached rows it may see, itself included.
+struct Query {
+  int s, len;
+};
+__device__ __forceinline__ Query query(const Params& p, int t) {
+  if (p.cu == nullptr) return Query{t, max(__ldg(p.kv.kv_len + t), 0)};
+  const int s = sequence_of(p.cu, p.kv.n_seq, t);
+  if (s < 0 || s >= p.kv.n_seq) return Query{-1, 0};
+  const int64_t len = (int64_t)max(__ldg(p.kv.kv_len + s), 0) - (__ldg(p.cu + s + 1) - 1 - t);
+  return Query{s, (int)min(max(len, (int64_t)0), (int64_t)INT32_MAX)};
+}
+
+// The cached rows a query sees: rows [0, first) and [lo, lo + n - first).
 struct Visible {
   int n, first, lo;
 };
-__device__ __forceinline__ Visible visible(const Params& p, int s) {
-  const int len = max(__ldg(p.kv.kv_len + s), 0);
-  const int held = min(len, p.kv.capacity);
-  const int lo = p.window > 0 ? min(max(len - p.window, 0), held) : 0;
+__device__ __forceinline__ Visible visible(const Params& p, const Query& q) {
+  const int held = min(q.len, p.kv.capacity);
+  const int lo = p.window > 0 ? min(max(q.len - p.window, 0), held) : 0;
   const int first = min(p.sinks, lo);
   return Visible{first + held - lo, first, lo};
 }
 
 // A unit's part: tiles [t0, t1) of its nt.
 struct Segment {
+  int t;            // query row
   int s, g, chunk;  // sequence, kv head, chunk of query heads
   int rows, h0;     // its query heads
   int t0, t1, nt;
@@ -184,7 +198,7 @@ __device__ void run_bf16(const Params& p, const Segment& sg, unsigned char* smem
 
   uint32_t qa[D / 16][4];
   {
-    const T* q = (const T*)p.q + (int64_t)sg.s * p.q_row;
+    const T* q = (const T*)p.q + (int64_t)sg.t * p.q_row;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
@@ -333,7 +347,7 @@ __device__ void run_f32(const Params& p, const Segment& sg, unsigned char* smem)
   for (int i = 0; i < C::kStages - 1; ++i) st.load(sg.t0 + i, i);
   for (int e = threadIdx.x; e < R * D; e += kThreads) {
     const int r = e / D;
-    qs[e] = r < sg.rows ? ((const float*)p.q)[(int64_t)sg.s * p.q_row + (int64_t)(sg.h0 + r) * p.q_head + e % D] : 0.f;
+    qs[e] = r < sg.rows ? ((const float*)p.q)[(int64_t)sg.t * p.q_row + (int64_t)(sg.h0 + r) * p.q_head + e % D] : 0.f;
   }
   __syncthreads();
   constexpr int NH = R >= 2 ? R / 2 : 1;  // heads of a lane
@@ -502,9 +516,9 @@ __device__ __forceinline__ void combine(const Params& p, const Segment& sg, int 
       if (c == 0) __stcg(reinterpret_cast<float2*>(to) + row, make_float2(M_, L));
     } else {
       const float inv = L == 0.f ? 0.f : 1.f / L;
-      store4<T>(p, (int64_t)(sg.h0 + row) * p.o_head + (int64_t)sg.s * p.o_row + c,
+      store4<T>(p, (int64_t)(sg.h0 + row) * p.o_head + (int64_t)sg.t * p.o_row + c,
                 make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
-      if (c == 0 && p.lse) p.lse[(int64_t)(sg.h0 + row) * p.kv.n_seq + sg.s] = row_lse(M_, L);
+      if (c == 0 && p.lse) p.lse[(int64_t)(sg.h0 + row) * p.n_rows + sg.t] = row_lse(M_, L);
     }
   }
 }
@@ -531,18 +545,18 @@ __device__ void run_segment(const Params& p, const Segment& sg, unsigned char* s
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) k_decode(const Params p) {
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ int sh_seq, sh_last;
+  __shared__ int sh_row, sh_last;
   __shared__ int64_t sh_sum[kWarps], sh_before;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n_seq = p.kv.n_seq;
-  // tiles in front of this thread's run of sequences
-  const int per = (n_seq + kThreads - 1) / kThreads;
-  const int s_lo = min(n_seq, (int)threadIdx.x * per), s_hi = min(n_seq, s_lo + per);
+  const int n_rows = p.n_rows;
+  // tiles in front of this thread's run of query rows
+  const int per = (n_rows + kThreads - 1) / kThreads;
+  const int t_lo = min(n_rows, (int)threadIdx.x * per), t_hi = min(n_rows, t_lo + per);
   int64_t mine = 0;
-  for (int s = s_lo; s < s_hi; ++s) {
-    const Visible v = visible(p, s);
-    mine += (v.n + kTile - 1) / kTile;
-    if (blockIdx.x == 0 && __ldg(p.kv.kv_len + s) > p.kv.capacity) set_status(p.ws, MR_ERR_DEVICE_CHECK, kTableShort);
+  for (int t = t_lo; t < t_hi; ++t) {
+    const Query q = query(p, t);
+    mine += (visible(p, q).n + kTile - 1) / kTile;
+    if (blockIdx.x == 0 && q.len > p.kv.capacity) set_status(p.ws, MR_ERR_DEVICE_CHECK, kTableShort);
   }
   int64_t upto = mine;
 #pragma unroll
@@ -562,45 +576,48 @@ __global__ void __launch_bounds__(kThreads) k_decode(const Params p) {
   const int HC = p.kv.H_kv * p.chunks;
   const int64_t total = tiles * HC;
   const int64_t ctas = min((int64_t)gridDim.x, total);
-  // sequences without visible rows
-  for (int s = blockIdx.x; s < n_seq; s += gridDim.x) {
-    if (visible(p, s).n > 0) continue;
+  // query rows that see nothing
+  for (int t = blockIdx.x; t < n_rows; t += gridDim.x) {
+    const Query q = query(p, t);
+    if (q.s < 0 || visible(p, q).n > 0) continue;
     for (int e = threadIdx.x; e < p.H_q * (D / 4); e += kThreads)
-      store4<T>(p, (int64_t)(e / (D / 4)) * p.o_head + (int64_t)s * p.o_row + 4 * (e % (D / 4)),
+      store4<T>(p, (int64_t)(e / (D / 4)) * p.o_head + (int64_t)t * p.o_row + 4 * (e % (D / 4)),
                 make_float4(0.f, 0.f, 0.f, 0.f));
     if (p.lse)
-      for (int h = threadIdx.x; h < p.H_q; h += kThreads) p.lse[(int64_t)h * n_seq + s] = -INFINITY;
+      for (int h = threadIdx.x; h < p.H_q; h += kThreads) p.lse[(int64_t)h * n_rows + t] = -INFINITY;
   }
   const int64_t k = blockIdx.x;
   if (k >= ctas) return;
   int64_t cur = k * total / ctas;
   const int64_t end = (k + 1) * total / ctas;
   if (cur >= before * HC && cur < (before + mine) * HC) {  // exactly one thread: the run that holds `cur`
-    int s = s_lo;
+    int t = t_lo;
     int64_t b = before;
-    for (;; ++s) {
-      const int nt = (visible(p, s).n + kTile - 1) / kTile;
+    for (;; ++t) {
+      const int nt = (visible(p, query(p, t)).n + kTile - 1) / kTile;
       if (cur < (b + nt) * HC) break;
       b += nt;
     }
-    sh_seq = s;
+    sh_row = t;
     sh_before = b;
   }
   __syncthreads();
-  int s = sh_seq;
+  int t = sh_row;
   int64_t b = sh_before;
   while (cur < end) {
     Segment sg;
-    sg.vis = visible(p, s);
+    const Query q = query(p, t);
+    sg.vis = visible(p, q);
     sg.nt = (sg.vis.n + kTile - 1) / kTile;
     if (cur >= (b + sg.nt) * HC) {
       b += sg.nt;
-      ++s;
+      ++t;
       continue;
     }
     const int64_t r = cur - b * HC;
     const int hu = (int)(r / sg.nt);
-    sg.s = s;
+    sg.t = t;
+    sg.s = q.s;
     sg.t0 = (int)(r - (int64_t)hu * sg.nt);
     sg.t1 = (int)min((int64_t)sg.nt, sg.t0 + (end - cur));
     sg.g = hu / p.chunks;
@@ -653,7 +670,7 @@ cudaError_t launch(const DecodeArgs& a, const Params& p, int sms) {
   if (e != cudaSuccess) return e;
   const int per_sm = smem <= 113 * 1024 ? 2 : 1;
   // no more CTAs than there can be tiles
-  const int64_t tiles = (int64_t)a.kv.n_seq * p.kv.H_kv * p.chunks * (((int64_t)a.kv.capacity + kTile - 1) / kTile);
+  const int64_t tiles = (int64_t)a.n_rows * p.kv.H_kv * p.chunks * (((int64_t)a.kv.capacity + kTile - 1) / kTile);
   int grid = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
   if (tiles < grid) grid = (int)tiles;
   ProfScope ps(kKDecode, a.stream);
@@ -684,6 +701,8 @@ cudaError_t launch_decode(const DecodeArgs& a) {
   p.o_head = a.o.head_stride;
   p.o_row = a.o.row_stride;
   p.lse = a.lse;
+  p.cu = a.cu_q;
+  p.n_rows = a.n_rows;
   p.H_q = a.H_q;
   p.group = a.H_q / a.kv.H_kv;
   p.chunks = (p.group + kMaxRows - 1) / kMaxRows;

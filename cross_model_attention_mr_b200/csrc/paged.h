@@ -54,6 +54,8 @@ struct RopeArgs {
 
 struct DecodeArgs {
   PagedKv kv;
+  const int32_t* cu_q;  // NULL: one row per sequence; otherwise rows of a chunk, each as a token of its own
+  int n_rows;
   mr_rows q, o;
   int H_q;
   mr_dtype dt;

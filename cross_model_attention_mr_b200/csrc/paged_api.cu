@@ -162,6 +162,8 @@ mr_status mr_paged_decode(const mr_kv_cache* cache, const mr_kv_seqs* seqs, cons
     return MR_ERR_INVALID_ARG;
   DecodeArgs a;
   a.kv = view(cache, seqs);
+  a.cu_q = nullptr;
+  a.n_rows = seqs->n_seq;
   a.q = *Q;
   a.o = *O;
   a.H_q = H_q;

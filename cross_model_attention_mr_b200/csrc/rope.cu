@@ -48,19 +48,6 @@ struct Params {
   WsHeader* ws;
 };
 
-// Sequence of packed row t: the s with cu[s] <= t < cu[s + 1]; n_seq behind the last one, -1 in front of the first.
-__device__ __forceinline__ int sequence_of(const int32_t* cu, int n_seq, int t) {
-  int lo = -1, hi = n_seq;  // cu[lo + 1] <= t or lo = -1; cu[hi] > t or hi = n_seq
-  while (hi - lo > 1) {
-    const int m = lo + (hi - lo) / 2;
-    if (__ldg(cu + m) <= t)
-      lo = m;
-    else
-      hi = m;
-  }
-  return lo < 0 ? -1 : (lo == n_seq - 1 && __ldg(cu + n_seq) <= t ? n_seq : lo);
-}
-
 template <typename T, int VEC, bool Append>
 __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ mr_rope rope, const __grid_constant__ Params p) {
   using V = Vec<T, VEC>;

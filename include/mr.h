@@ -555,7 +555,8 @@ mr_status mr_paged_decode(const mr_kv_cache* cache, const mr_kv_seqs* seqs, cons
  *   lse  NULL or device fp32 [H_q][total_q]
  * A row that sees nothing (a negative position) gets O = 0 and lse = -inf.  Rows of the cache that a new
  * row does not see do not influence its result, whatever they hold.  Probabilities enter the second
- * product in the cache's type (bf16: off by at most 2^-8 of themselves); sums are fp32.
+ * product in the cache's type (bf16: off by at most 2^-8 of themselves; calls of few rows, which run as
+ * mr_paged_decode does: 2^-16); sums are fp32.
  */
 mr_status mr_paged_attn(const mr_kv_cache* cache, const mr_kv_seqs* seqs, const mr_rows* Q, int H_q,
                         const int32_t* cu_q, int total_q, float scale, int window, int sinks,

@@ -271,15 +271,30 @@ def test_attn_many_units_and_parts(mr, dt, d):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_attn_many_sequences(mr, dt):
-    """More runs of new rows than a CTA has threads, some without rows, some that hold nothing."""
+@pytest.mark.parametrize("most", [2, 5])
+def test_attn_many_sequences(mr, dt, most):
+    """More runs of new rows than a CTA has threads, some without rows, some that hold nothing (most 2: fewer rows than
+    sequences)."""
     rng = np.random.default_rng(2)
-    new = rng.integers(0, 3, 1300)
+    new = rng.integers(0, most, 1300)
     held = np.maximum(new + rng.integers(-1, 40, 1300), 0)
     new[:5], held[700:705] = 0, 0
     c = Case(mr, new.tolist(), held.tolist(), 2, 1, 16, 64, dt, seed=16)
     O, lse = mr.paged_attn(*c.args(), c.cu, window=20, sinks=2, return_lse=True, ws=c.ws)
     c.check(O, lse, window=20, sinks=2, p_eps=ATTN_P[dt])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("new,held,p", [([7], [7], DECODE_P), ([4, 0, 3], [2, 5, 600], DECODE_P),
+                                        # 41 rows (one behind the last) of 40 sequences: worked on in tiles, P is one part
+                                        ([1] * 40, list(range(40)), ATTN_P),
+                                        ([1] * 40 + [0], list(range(40)) + [3], DECODE_P), ([8], [5000], DECODE_P)])
+def test_attn_of_few_rows(mr, dt, new, held, p):
+    """Rows that are worked on one by one, each with its own end and window."""
+    c = Case(mr, new, held, 12, 3, 16, 128, dt, seed=19, behind=1)
+    for window, sinks in ((0, 0), (5, 0), (30, 7)):
+        O, lse = mr.paged_attn(*c.args(), c.cu, window=window, sinks=sinks, return_lse=True, ws=c.ws)
+        c.check(O, lse, window=window, sinks=sinks, p_eps=p[dt])
 
 
 def test_two_calls_at_once(mr):
