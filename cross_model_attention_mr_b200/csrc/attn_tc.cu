@@ -84,7 +84,8 @@ __device__ __forceinline__ void fail(Smem<D>& s, const AttnParams& p, uint32_t d
   s.abort = 1;
 }
 
-// mbar_wait by a whole warp for the phase with `n`'s parity: all lanes go on, or none.
+// mbar_wait by a whole warp for the phase with `n`'s parity: all lanes go on, or none.  All of them wait: a form in which
+// one lane did and the others met it at the vote faulted.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t n, const volatile int* abort, uint64_t ns) {
   return __all_sync(0xffffffffu, mbar_wait(bar, n & 1, abort, ns));
 }
