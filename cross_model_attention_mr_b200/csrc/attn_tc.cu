@@ -100,12 +100,6 @@ __device__ __forceinline__ bool on_edge(int window, int sinks, int first, int la
 // Bits 0 .. n - 1, for any n.
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u; }
 
-// Mask of the bf16 halves of w that are infinite or NaN (an exponent of all ones carries into the bit above when one is
-// added to it).
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-  return ((((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) >> 15) * 0xffffu;
-}
-
 // Key tiles of the segment that tile x of the unit needs (a front part of them), 0 for a missing tile.
 __device__ __forceinline__ int steps_of(const AttnParams& p, const Seg& sg, int x) {
   if (x * p.tile_tokens >= sg.u.n) return 0;

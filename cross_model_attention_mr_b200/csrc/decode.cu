@@ -17,7 +17,9 @@
 // needs no more, and the 128-row tcgen05 tile would be filled to an eighth.  The scores' registers are the
 // second product's operand as they are.  Probabilities are split into two bf16 parts (value and remainder)
 // so that their rounding does not show beside the output's own; with up to 8 heads both parts share one
-// instruction (rows 0-7 and 8-15).  fp32 runs on the CUDA cores.
+// instruction (rows 0-7 and 8-15).  A remainder may be 0 or negative, so an infinite value must not meet it: a warp
+// whose sums come out infinite or NaN reads its rows a second time and leaves such values out of that product.  fp32
+// runs on the CUDA cores.
 // 8 sequences of 32768 rows, 64 heads in groups of 8 (1.07 GB): 173 us, 6.2 TB/s, 94% of a copy's rate; 16 sequences of
 // 4608 to 6144 rows, 32 heads in groups of 4: 63 us, 5.6 TB/s.
 #include <cuda_bf16.h>
@@ -184,9 +186,11 @@ struct Stream {  // one warp's slices of a segment
 };
 
 // ---- bf16 ----------------------------------------------------------------------------------------
-// Warp state of a segment: lane holds, of query heads lane / 4 (and + 8), the output columns 8 n + 2 (lane % 4) + {0, 1}.
-template <int D, bool Half>
-__device__ void run_bf16(const Params& p, const Segment& sg, unsigned char* smem) {
+// A warp's slices of a segment: lane holds, of query heads lane / 4 (and + 8), maxima m, its share of the sums l, and the
+// output columns 8 n + 2 (lane % 4) + {0, 1}.  Careful: values that are not finite meet the rounded probabilities only.
+template <int D, bool Half, bool Careful>
+__device__ __forceinline__ void slices_bf16(const Params& p, const Segment& sg, unsigned char* smem, float (&o)[D / 8][4],
+                                            float (&m)[2], float (&l)[2]) {
   using T = __nv_bfloat16;
   using C = Cfg<T, D>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -217,10 +221,10 @@ __device__ void run_bf16(const Params& p, const Segment& sg, unsigned char* smem
         }
       }
   }
-  float o[D / 8][4];
 #pragma unroll
   for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  m[0] = m[1] = -INFINITY;
+  l[0] = l[1] = 0.f;
   constexpr int NR = Half ? 1 : 2;
 
   const int mi = lane >> 3, mr = lane & 7;  // the 8x8 matrix and its row that this lane addresses
@@ -297,15 +301,65 @@ __device__ void run_bf16(const Params& p, const Segment& sg, unsigned char* smem
       uint32_t b[4];
       const int r = (mi & 1) * 8 + mr, ch = 2 * dd + (mi >> 1);
       ldsm4_t(vb + r * C::kRowBytes + ((ch ^ (r & 7)) << 4), b);
-      mma16816(o[2 * dd], pa, b[0], b[1]);
-      mma16816(o[2 * dd + 1], pa, b[2], b[3]);
-      if (!Half) {
-        mma16816(o[2 * dd], pl, b[0], b[1]);
-        mma16816(o[2 * dd + 1], pl, b[2], b[3]);
+      if (!Careful) {
+        mma16816(o[2 * dd], pa, b[0], b[1]);
+        mma16816(o[2 * dd + 1], pa, b[2], b[3]);
+        if (!Half) {
+          mma16816(o[2 * dd], pl, b[0], b[1]);
+          mma16816(o[2 * dd + 1], pl, b[2], b[3]);
+        }
+      } else {
+        const uint32_t hi[4] = {pa[0], Half ? 0u : pa[1], pa[2], Half ? 0u : pa[3]};
+        const uint32_t rest[4] = {Half ? 0u : pl[0], Half ? pa[1] : pl[1], Half ? 0u : pl[2], Half ? pa[3] : pl[3]};
+#pragma unroll
+        for (int c8 = 0; c8 < 2; ++c8) {
+          float(&x)[4] = o[2 * dd + c8];
+          const uint32_t b0 = b[2 * c8], b1 = b[2 * c8 + 1];
+          float y[4] = {x[0], x[1], Half ? 0.f : x[2], Half ? 0.f : x[3]};
+          mma16816(y, hi, b0, b1);
+          x[0] = y[0];
+          x[1] = y[1];
+          if (!Half) {
+            x[2] = y[2];
+            x[3] = y[3];
+          }
+          mma16816(x, rest, b0 & ~not_finite(b0), b1 & ~not_finite(b1));
+        }
       }
     }
   }
   cp_wait<0>();
+}
+
+// (a function of its own, with results of its own: the ordinary pass keeps its registers)
+template <int D, bool Half>
+__device__ __noinline__ void slices_bf16_again(const Params& p, const Segment sg, unsigned char* smem,
+                                               float (&o)[D / 8][4]) {
+  float m[2], l[2];
+  slices_bf16<D, Half, true>(p, sg, smem, o, m, l);
+}
+
+template <int D, bool Half>
+__device__ void run_bf16(const Params& p, const Segment& sg, unsigned char* smem) {
+  constexpr int NR = Half ? 1 : 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c2 = 2 * (lane & 3);
+  float o[D / 8][4], m[2], l[2];
+  slices_bf16<D, Half, false>(p, sg, smem, o, m, l);
+  float zero[4] = {0.f, 0.f, 0.f, 0.f};  // stays 0 while every output is finite
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) zero[e] = fmaf(o[n][e], 0.f, zero[e]);
+  if (__any_sync(0xffffffffu, !(zero[0] + zero[1] + zero[2] + zero[3] == 0.f))) {
+    float again[D / 8][4];
+    __syncwarp();
+    slices_bf16_again<D, Half>(p, sg, smem, again);
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = again[n][e];
+  }
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -543,7 +597,7 @@ __device__ void run_segment(const Params& p, const Segment& sg, unsigned char* s
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) k_decode(const Params p) {
+__global__ void __launch_bounds__(kThreads) k_decode(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ int sh_row, sh_last;
   __shared__ int64_t sh_sum[kWarps], sh_before;

@@ -23,6 +23,12 @@ __device__ __forceinline__ int pool_row(const PagedKv& kv, int s, int g, int j) 
   return (page * kv.H_kv + g) * kv.page_rows + (j - pi * kv.page_rows);
 }
 
+// Mask of the bf16 halves of w that are infinite or NaN (an exponent of all ones carries into the bit above when one is
+// added to it).
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  return ((((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) >> 15) * 0xffffu;
+}
+
 // Sequence of packed row t: the s with cu[s] <= t < cu[s + 1]; n_seq behind the last one, -1 in front of the first.
 __device__ __forceinline__ int sequence_of(const int32_t* cu, int n_seq, int t) {
   int lo = -1, hi = n_seq;  // cu[lo + 1] <= t or lo = -1; cu[hi] > t or hi = n_seq
