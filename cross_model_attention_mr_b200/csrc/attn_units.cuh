@@ -269,24 +269,32 @@ __device__ __forceinline__ void holders(const Share& sh, const Seg& sg, int& fir
 // and one that began before, at most).
 __device__ __forceinline__ int64_t slot_of(int c, int first) { return 2 * (int64_t)c + (c == first ? 1 : 0); }
 
-// Rows that see nothing because the sequence holds fewer rows than its new ones, and lengths beyond the table.
+// Rows that see nothing, where no unit need take them: negative positions (the sequence holds fewer rows than its new
+// ones), and without sinks those whose window begins behind the last row that the table covers.  Lengths beyond the table
+// are recorded.
 template <typename T, int D, int NT>
 __device__ void empty_rows(const AttnParams& p) {
   for (int s = blockIdx.x; s < p.kv.n_seq; s += gridDim.x) {
     int q0, n;
     seq_rows(p, s, q0, n);
     const int len = max(__ldg(p.kv.kv_len + s), 0);
+    const int held = min(len, p.kv.capacity);
     if (n > 0 && len > p.kv.capacity && threadIdx.x == 0) set_status(p.ws, MR_ERR_DEVICE_CHECK, kTableShort);
-    const int64_t m = len < n ? n - len : 0;
+    // the first `front` rows and the last `behind` (a position from held + window - 1 on sees nothing)
+    const int front = min(max(n - len, 0), n);
+    const int64_t late = p.window > 0 && p.sinks == 0 ? (int64_t)len - held - p.window + 1 : 0;
+    const int behind = (int)min(max(late, (int64_t)0), (int64_t)(n - front));
+    const int64_t m = front + behind;
+    const auto row_of = [&](int i) { return q0 + (i < front ? i : n - behind + (i - front)); };
     for (int64_t e = threadIdx.x; e < m * p.H_q * D; e += NT) {
       const int64_t hr = e / D;
-      const int h = (int)(hr / m), row = q0 + (int)(hr - (int64_t)h * m);
+      const int h = (int)(hr / m), row = row_of((int)(hr - (int64_t)h * m));
       ((T*)p.o)[(int64_t)h * p.o_head + (int64_t)row * p.o_row + e % D] = from_f32<T>(0.f);
     }
     if (p.lse)
       for (int64_t e = threadIdx.x; e < m * p.H_q; e += NT) {
         const int h = (int)(e / m);
-        p.lse[(int64_t)h * p.total_q + q0 + (e - (int64_t)h * m)] = -INFINITY;
+        p.lse[(int64_t)h * p.total_q + row_of((int)(e - (int64_t)h * m))] = -INFINITY;
       }
   }
 }

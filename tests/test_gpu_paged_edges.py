@@ -63,3 +63,41 @@ def test_attn_gives_infinities_to_the_rows_that_see_them(mr, dt, new):
         assert bool((got[:, seen, col] == x).all()) and bool(torch.isfinite(got[:, ~seen, col]).all())
         got[:, seen, col] = want[:, seen, col]
     c.check(got, gl, window=50, p_eps=(DECODE_P if new <= 8 else ATTN_P)[dt])
+
+
+# ---------------------------------------------------------------------------------------------- short tables
+@pytest.mark.parametrize("dt,pr", [("bf16", 16), ("bf16", 12), ("f32", 16)])
+@pytest.mark.parametrize("new,held,pages", [(300, 400, 4), (300, 330, 4), (40, 600, 2), (12, 600, 2), (600, 600, 1)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (10, 0), (200, 0), (10, 3)])
+def test_rows_behind_a_short_table_see_nothing(mr, dt, pr, new, held, pages, window, sinks):
+    """A length beyond the table: rows whose whole window lies behind it are written as rows that see nothing."""
+    Hq, Hk, d = 4, 2, 64
+    c = Case(mr, [new, 30], [held, 30], Hq, Hk, pr, d, dt, seed=23)
+    cache, table, lens, q = c.args()
+    table = table[:, :max(pages, -(-30 // pr))].contiguous()
+    cap = table.shape[1] * pr
+    O = torch.full_like(q, 5.0)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    mr.paged_attn(cache, table, lens, q, c.cu, window=window, sinks=sinks, out=O, lse=lse, ws=c.ws)
+    assert c.ws.sync_status() == mr.MR_ERR_DEVICE_CHECK
+    scale = float(np.float32(1 / math.sqrt(d)))
+    pos = np.concatenate([np.arange(held - new, held), np.arange(30)])
+    seq = np.repeat([0, 1], [new, 30])
+    O, lse, Q = np64(O), np64(lse), np64(q)
+    eps = torch.finfo(DT[dt]).eps
+    few = new + 30 <= (16 if dt == "bf16" else 8)
+    for i, (s, p) in enumerate(zip(seq, pos)):
+        j = np.arange(min(p + 1, cap))
+        j = j[(j > p - window) | (j < sinks)]
+        if len(j) == 0:
+            assert np.all(O[:, i] == 0) and np.all(lse[:, i] == -np.inf), (i, p)
+            continue
+        pages_, rows = c.table.numpy()[s, j // pr], j % pr
+        for h in range(Hq):
+            K, V = c.clean_k[pages_, h // 2, rows], c.clean_v[pages_, h // 2, rows]
+            x = scale * (K @ Q[h, i])
+            w = np.exp(x - x.max())
+            want, wl = w @ V / w.sum(), x.max() + np.log(w.sum())
+            A, S = w @ np.abs(V) / w.sum(), scale * (np.abs(K) @ np.abs(Q[h, i])).max()
+            tol, ltol = attend_tol(want, np.float64(wl), A, np.float64(S), d, len(j), eps, ATTN_P[dt])
+            assert np.all(np.abs(O[h, i] - want) <= tol) and abs(lse[h, i] - wl) <= ltol, (i, p, h)
