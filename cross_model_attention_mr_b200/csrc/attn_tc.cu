@@ -576,7 +576,8 @@ struct Steps {
 // Scores of keys 64 h .. at Tensor Memory column 256 x + 64 h, all of P in the first half's columns.  The second half
 // is worked on first: its scores are computed while the previous step's P is still being made, so its exponentials run
 // during the products that the first half's scores wait for.  They use the reference as it stands; where the first half
-// then moves it (in a segment's first steps, hardly later), P of the second half is scaled, at most 2^-8, and rounded again.
+// then moves it (in a segment's first steps, hardly later), P of the second half is scaled.  That move goes by whole
+// steps, so the factor is a power of two and P is not rounded a second time.
 template <int D>
 __device__ __noinline__ bool softmax_steps(Smem<D>& s, const Steps t, float& ref_out, float& l_out) {
   // (copies that no memory clobber makes the compiler read again)
@@ -639,12 +640,22 @@ __device__ __noinline__ bool softmax_steps(Smem<D>& s, const Steps t, float& ref
     l += sum[0].x + sum[0].y;
   };
   // The reference moves to the row maximum at the first finite score (so a row that sees one key gives it exactly 1) and
-  // whenever a score passes it by more than 2^8; returns whether one of the warp's rows did, and what its sums have to be multiplied by.
-  auto move = [&](float mt, float& f) {
+  // whenever a score passes it by more than 2^8, with `whole` to the next whole step above that; returns whether one of the
+  // warp's rows did, and what its sums have to be multiplied by.
+  auto move = [&](float mt, float& f, bool whole) {
     const bool need = ref == -INFINITY ? mt > -INFINITY : mt - ref > kRescale;
     if (!__any_sync(0xffffffffu, need)) return false;
-    f = !need ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx(ref - mt));
-    if (need) ref = mt;
+    f = 1.f;
+    if (need) {
+      const float by = ceilf(mt - ref);  // (infinite at the first finite score)
+      if (whole && by < 126.f) {
+        f = __int_as_float((127 - (int)by) << 23);
+        ref += by;
+      } else {
+        f = ref == -INFINITY ? 0.f : ex2_approx(ref - mt);  // (where `whole`: too small to count, however it is rounded)
+        ref = mt;
+      }
+    }
     l *= f;
     return true;
   };
@@ -660,7 +671,7 @@ __device__ __noinline__ bool softmax_steps(Smem<D>& s, const Steps t, float& ref
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.s_read[x]);
-    if (move(mh, f) && j > 0) {
+    if (move(mh, f, false) && j > 0) {
       // (the first half's scores are computed behind the last product that adds to O)
       if (!warp_wait(&s_full[0], sc + j, &s.abort, wait_ns)) return false;
       tc_fence_after();
@@ -670,7 +681,7 @@ __device__ __noinline__ bool softmax_steps(Smem<D>& s, const Steps t, float& ref
     if (!warp_wait(&s_full[0], sc + j, &s.abort, wait_ns)) return false;
     tc_fence_after();
     const float ml = load(0, key0);
-    if (move(ml, f)) {
+    if (move(ml, f, true)) {
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
         const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&ph[e]));

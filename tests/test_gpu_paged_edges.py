@@ -101,3 +101,54 @@ def test_rows_behind_a_short_table_see_nothing(mr, dt, pr, new, held, pages, win
             A, S = w @ np.abs(V) / w.sum(), scale * (np.abs(K) @ np.abs(Q[h, i])).max()
             tol, ltol = attend_tol(want, np.float64(wl), A, np.float64(S), d, len(j), eps, ATTN_P[dt])
             assert np.all(np.abs(O[h, i] - want) <= tol) and abs(lse[h, i] - wl) <= ltol, (i, p, h)
+
+
+# ---------------------------------------------------------------------------------------------- moving references
+def test_attn_rounds_probabilities_once(mr):
+    """The second half of the first key tile holds scores 0 and -e, the first half one of s > 8 (in base 2): the reference
+    moves after the second half's probabilities were made.  63 equal ones carry the output's only values, so a second
+    rounding of them would show: rounded twice, 172 of these shifts would put some row beyond half a step of the
+    probabilities and half a step of the output."""
+    shifts, es = 8 + np.arange(1, 256) / 32, np.arange(1, 512) / 256
+    new = 510
+    d, past = 64, 128
+    e = es[:new]
+    for at in range(0, len(shifts), 8):
+        Hq = min(8, len(shifts) - at)
+        c = Case(mr, [new], [past + new], Hq, 1, 16, d, "bf16", seed=24)
+        c.q.zero_()
+        for x, y in ((c.k, c.clean_k), (c.v, c.clean_v)):
+            live = torch.isfinite(x)
+            x.masked_fill_(live, 0.0)
+            y[:] = 0.0
+
+        def put(t, clean, row, col, x):
+            t[c.table[0, row // 16], 0, row % 16, col] = x
+            clean[int(c.table[0, row // 16]), 0, row % 16, col] = x
+        for h in range(Hq):
+            s = shifts[at + h]
+            c.q[h, :new, 0] = math.floor(s)
+            c.q[h, :new, 1] = s - math.floor(s)
+        c.q[:, :new, 2] = torch.from_numpy(np.floor(e)).bfloat16().cuda()
+        c.q[:, :new, 3] = torch.from_numpy(e - np.floor(e)).bfloat16().cuda()
+        put(c.k, c.clean_k, 5, 0, 1.0)
+        put(c.k, c.clean_k, 5, 1, 1.0)
+        for row in range(65, 128):
+            put(c.k, c.clean_k, row, 2, -1.0)
+            put(c.k, c.clean_k, row, 3, -1.0)
+            put(c.v, c.clean_v, row, 7, 1.0)
+        assert np.array_equal(np64(c.q)[0, :new, 2] + np64(c.q)[0, :new, 3], e)
+        O, lse = mr.paged_attn(*c.args(), c.cu, scale=math.log(2.0), window=1, sinks=128, return_lse=True, ws=c.ws)
+        # (scores are sums of two products of small fractions: exact, but for the scale; the bound's terms for them are
+        # far below the rounding's)
+        Q, scale = np64(c.q)[:, :new], float(np.float32(math.log(2.0)))
+        top, low = scale * (Q[..., 0] + Q[..., 1]), -scale * (Q[..., 2] + Q[..., 3])
+        # 63 + 1 keys at 0 in the first tile and the row's own, one at `top`, 63 at `low`
+        total = 65 + np.exp(top) + 63 * np.exp(low)
+        want = 63 * np.exp(low) / total
+        tol, ltol = attend_tol(want[..., None], np.log(total), want[..., None], top, d, 129, torch.finfo(torch.bfloat16).eps,
+                               2.0 ** -8)
+        err = np.abs(np64(O)[:, :new, 7] - want)
+        assert np.all(err <= tol[..., 0]), float((err / tol[..., 0]).max())
+        assert np.all(np.abs(np64(lse)[:, :new] - np.log(total)) <= ltol)
+        assert c.ws.sync_status() == mr.MR_OK
