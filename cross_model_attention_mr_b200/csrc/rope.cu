@@ -59,6 +59,8 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ mr_ro
   const int within = (int)(id - slab * ((int64_t)upr << 20));
   const int t_in = (int)fast_div((uint32_t)within, p.by_units), i = within - t_in * upr;
   const int t = (int)(slab << 20) + t_in;
+  // rows in front of the first sequence and behind the last one are not read
+  if (Append && p.cu && (t < __ldg(p.cu) || t >= __ldg(p.cu + p.kv.n_seq))) return;
   const int half = p.rot >> 1, rotated = half / VEC;
   // the unit's two vectors: the halves of its pairs, or neighbours
   const bool split = i < rotated && !p.interleaved;

@@ -152,3 +152,34 @@ def test_attn_rounds_probabilities_once(mr):
         assert np.all(err <= tol[..., 0]), float((err / tol[..., 0]).max())
         assert np.all(np.abs(np64(lse)[:, :new] - np.log(total)) <= ltol)
         assert c.ws.sync_status() == mr.MR_OK
+
+
+# ---------------------------------------------------------------------------------------------- more rows than there are
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_append_with_an_upper_bound_of_the_rows(mr, dt):
+    """total_q may be an upper bound: tensors that end with the last sequence's rows are enough.  (Theirs lie in front of a
+    larger allocation here, so that nothing else is in reach of rows behind them.)"""
+    import ctypes
+    T, most, Hq, Hk, d, pr = 37, 5000, 4, 2, 64, 16
+    each = Hq + 2 * Hk
+    x = torch.full((most, each, d), math.nan, dtype=DT[dt], device="cuda")
+    x[:T] = rand((T, each, d), dt, 25)
+    out = torch.full((most, Hq, d), 5.0, dtype=DT[dt], device="cuda")
+    lens = torch.tensor([20, 60], dtype=torch.int32).cuda()
+    cu = torch.tensor([0, 12, T], dtype=torch.int32).cuda()
+    table = torch.arange(8, dtype=torch.int32).view(2, 4).cuda()
+    a, b = (mr.KVCache(torch.full((8, Hk, pr, d), 9.0, dtype=DT[dt], device="cuda"),
+                       torch.full((8, Hk, pr, d), -9.0, dtype=DT[dt], device="cuda")) for _ in range(2))
+    r, ws = mr.Rope(d), mr.Workspace(256)
+    esize = x.element_size()
+    rows = lambda t, head, heads: mr.Rows(t.data_ptr() + head * d * esize, d, heads * d)
+    seqs = mr.KvSeqs(table.data_ptr(), lens.data_ptr(), 4, 2)
+    ref = ctypes.byref
+    st = mr.LIB.mr_kv_append(ref(a.c), ref(seqs), ref(r.c), ref(rows(x, 0, each)), ref(rows(out, 0, Hq)), Hq,
+                             ref(rows(x, Hq, each)), ref(rows(x, Hq + Hk, each)), cu.data_ptr(), most, ws.ptr, ws.nbytes,
+                             torch.cuda.current_stream().cuda_stream)
+    assert st == mr.MR_OK and ws.sync_status() == mr.MR_OK
+    q, k, v = (t.transpose(0, 1) for t in x[:T].split([Hq, Hk, Hk], 1))
+    want = mr.kv_append(b, table, lens, k, v, cu_q=cu, rope=r, Q=q)
+    assert torch.equal(out[:T].transpose(0, 1), want) and bool((out[T:] == 5.0).all())
+    assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
