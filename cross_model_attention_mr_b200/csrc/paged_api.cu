@@ -15,6 +15,9 @@ mr_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MR_OK : MR_ERR_CU
 
 constexpr int kMaxHeads = 1024;
 
+// An address that is there and that the kernels may read and write in steps of `bytes`.
+bool aligned(const void* p, uintptr_t bytes) { return p && (uintptr_t)p % bytes == 0; }
+
 mr_status cache_ok(const mr_kv_cache* c) {
   if (!c) return MR_ERR_INVALID_ARG;
   if (c->dt != MR_BF16 && c->dt != MR_F32) return MR_ERR_UNSUPPORTED;
@@ -27,12 +30,12 @@ mr_status cache_ok(const mr_kv_cache* c) {
 }
 
 mr_status pools_ok(const mr_kv_cache* c) {
-  if (!c->k || !c->v || ((uintptr_t)c->k & 15u) || ((uintptr_t)c->v & 15u)) return MR_ERR_INVALID_ARG;
-  return MR_OK;
+  return aligned(c->k, 16) && aligned(c->v, 16) ? MR_OK : MR_ERR_INVALID_ARG;
 }
 
 mr_status seqs_ok(const mr_kv_seqs* s) {
-  if (!s || !s->table || !s->kv_len || s->pages_per_seq < 1 || s->n_seq < 1) return MR_ERR_INVALID_ARG;
+  if (!s || !aligned(s->table, 4) || !aligned(s->kv_len, 4) || s->pages_per_seq < 1 || s->n_seq < 1)
+    return MR_ERR_INVALID_ARG;
   return MR_OK;
 }
 
@@ -90,7 +93,7 @@ mr_status mr_rope_apply(const mr_rope* rope, const mr_rows* X, const mr_rows* Y,
   if (!rope_ok(rope) || H < 1 || n_rows < 0) return MR_ERR_INVALID_ARG;
   if (H > kMaxHeads) return MR_ERR_UNSUPPORTED;
   if (n_rows == 0) return MR_OK;
-  if (!pos) return MR_ERR_INVALID_ARG;
+  if (!aligned(pos, 4)) return MR_ERR_INVALID_ARG;
   if (!rows_ok(X, H, n_rows, rope->d, esize(dt), false) || !rows_ok(Y, H, n_rows, rope->d, esize(dt), true))
     return MR_ERR_INVALID_ARG;
   if (X->ptr == Y->ptr && ((H > 1 && X->head_stride != Y->head_stride) || (n_rows > 1 && X->row_stride != Y->row_stride)))
@@ -111,8 +114,8 @@ mr_status mr_kv_append(const mr_kv_cache* cache, const mr_kv_seqs* seqs, const m
                        void* stream) {
   mr_status e;
   if ((e = cache_ok(cache)) != MR_OK || (e = pools_ok(cache)) != MR_OK || (e = seqs_ok(seqs)) != MR_OK) return e;
-  if (!ws || ws_bytes < kWsHeaderBytes || total_q < 0) return MR_ERR_INVALID_ARG;
-  if (!cu_q && total_q != seqs->n_seq) return MR_ERR_INVALID_ARG;
+  if (!aligned(ws, 16) || ws_bytes < kWsHeaderBytes || total_q < 0) return MR_ERR_INVALID_ARG;
+  if (cu_q ? !aligned(cu_q, 4) : total_q != seqs->n_seq) return MR_ERR_INVALID_ARG;
   if (rope && (!rope_ok(rope) || rope->d != cache->d)) return MR_ERR_INVALID_ARG;
   if ((Q == nullptr) != (Q_out == nullptr)) return MR_ERR_INVALID_ARG;
   const int es = esize(cache->dt), d = cache->d;
@@ -158,7 +161,8 @@ mr_status mr_paged_decode(const mr_kv_cache* cache, const mr_kv_seqs* seqs, cons
   const int es = esize(cache->dt), d = cache->d;
   if (!rows_ok(Q, H_q, seqs->n_seq, d, es, false) || !rows_ok(O, H_q, seqs->n_seq, d, es, true))
     return MR_ERR_INVALID_ARG;
-  if (!ws || ((uintptr_t)ws & 15u) || ws_bytes < mr_paged_workspace_bytes(cache, H_q, seqs->n_seq))
+  if (lse && !aligned(lse, 4)) return MR_ERR_INVALID_ARG;
+  if (!aligned(ws, 16) || ws_bytes < mr_paged_workspace_bytes(cache, H_q, seqs->n_seq))
     return MR_ERR_INVALID_ARG;
   DecodeArgs a;
   a.kv = view(cache, seqs);
@@ -184,11 +188,12 @@ mr_status mr_paged_attn(const mr_kv_cache* cache, const mr_kv_seqs* seqs, const 
   if ((e = cache_ok(cache)) != MR_OK || (e = pools_ok(cache)) != MR_OK || (e = seqs_ok(seqs)) != MR_OK) return e;
   if (H_q < 1 || H_q % cache->H_kv || window < 0 || sinks < 0 || !isfinite(scale)) return MR_ERR_INVALID_ARG;
   if (H_q > kMaxHeads) return MR_ERR_UNSUPPORTED;
-  if (!cu_q || total_q < 0) return MR_ERR_INVALID_ARG;
+  if (!aligned(cu_q, 4) || total_q < 0) return MR_ERR_INVALID_ARG;
   const int es = esize(cache->dt), d = cache->d;
   if (total_q > 0 && (!rows_ok(Q, H_q, total_q, d, es, false) || !rows_ok(O, H_q, total_q, d, es, true)))
     return MR_ERR_INVALID_ARG;
-  if (!ws || ((uintptr_t)ws & 15u) || ws_bytes < mr_paged_workspace_bytes(cache, H_q, seqs->n_seq))
+  if (lse && !aligned(lse, 4)) return MR_ERR_INVALID_ARG;
+  if (!aligned(ws, 16) || ws_bytes < mr_paged_workspace_bytes(cache, H_q, seqs->n_seq))
     return MR_ERR_INVALID_ARG;
   AttnArgs a;
   a.kv = view(cache, seqs);
@@ -213,10 +218,10 @@ mr_status mr_pages_copy(void* const* pools, int n_pools, int64_t page_bytes, int
                         const int32_t* pairs, int n_pairs, void* ws, size_t ws_bytes, void* stream) {
   if (!pools || n_pools < 1 || page_bytes < 16 || page_bytes % 16 || n_pages < 1 || n_pairs < 0)
     return MR_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < kWsHeaderBytes || (n_pairs > 0 && !pairs)) return MR_ERR_INVALID_ARG;
+  if (!aligned(ws, 16) || ws_bytes < kWsHeaderBytes || (n_pairs > 0 && !aligned(pairs, 4))) return MR_ERR_INVALID_ARG;
   if (n_pages > INT32_MAX || page_bytes > ((int64_t)1 << 40)) return MR_ERR_UNSUPPORTED;
   for (int i = 0; i < n_pools; ++i)
-    if (!pools[i] || ((uintptr_t)pools[i] & 15u)) return MR_ERR_INVALID_ARG;
+    if (!aligned(pools[i], 16)) return MR_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   if (reset_header(ws, st) != cudaSuccess) return MR_ERR_CUDA;
   if (n_pairs == 0) return MR_OK;

@@ -505,9 +505,10 @@ mr_status mr_rope_apply(const mr_rope* rope, const mr_rows* X, const mr_rows* Y,
                         int n_rows, const int32_t* pos, int adjoint, void* stream);
 
 /* Workspace bytes of mr_kv_append, mr_paged_decode and mr_paged_attn for a cache, H_q query heads and
- * n_seq sequences (device memory, 256-byte aligned).  0 for an unsupported shape.  The contents need
- * not be set before a call nor kept after it, but for the status word; calls that can be under way at
- * the same time (on other streams, or in graphs replayed side by side) need a workspace each. */
+ * n_seq sequences (device memory, 256-byte aligned; an address that is no multiple of 16 is refused).
+ * 0 for an unsupported shape.  The contents need not be set before a call nor kept after it, but for
+ * the status word; calls that can be under way at the same time (on other streams, or in graphs
+ * replayed side by side) need a workspace each. */
 size_t mr_paged_workspace_bytes(const mr_kv_cache* cache, int H_q, int n_seq);
 
 /*
@@ -562,7 +563,7 @@ mr_status mr_paged_attn(const mr_kv_cache* cache, const mr_kv_seqs* seqs, const 
                         const int32_t* cu_q, int total_q, float scale, int window, int sinks,
                         const mr_rows* O, float* lse, void* ws, size_t ws_bytes, void* stream);
 
-/* Workspace bytes mr_pages_copy needs. */
+/* Workspace bytes mr_pages_copy needs (device memory, aligned as above). */
 size_t mr_pages_copy_workspace_bytes(void);
 
 /*
