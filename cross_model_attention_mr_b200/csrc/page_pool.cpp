@@ -18,6 +18,7 @@ namespace {
 struct Seq {
   std::vector<int32_t> pages;  // -1: given up by mr_pp_slide
   int rows = 0;
+  int window = 0, sinks = 0;   // of the last mr_pp_slide (window 0: none)
 };
 
 }  // namespace
@@ -44,10 +45,18 @@ struct mr_page_pool {
   void drop(int32_t page) {
     if (page >= 0 && --refs[page] == 0) put_free(page);
   }
-  // whether `s` can be cut to `rows`: the page of the last remaining row was not given up (so a page that
-  // new rows continue in is always there)
+  // whether `s` can be cut to `rows`: no page was given up that the next query (position `rows` or later, under the
+  // last slide's window and sinks) sees, nor the page of the last remaining row (so a page that new rows continue in
+  // is always there)
   bool can_end_at(const Seq& s, int rows) const {
-    return rows <= s.rows && (rows == 0 || rows == s.rows || s.pages[(rows - 1) / page_rows] >= 0);
+    if (rows > s.rows) return false;
+    if (rows == 0 || rows == s.rows) return true;
+    const int last = (rows - 1) / page_rows;
+    if (s.pages[last] < 0) return false;
+    const int64_t first = (int64_t)rows - s.window + 1;  // of the window
+    for (int i = 0; i < last; ++i)
+      if (s.pages[i] < 0 && ((int64_t)(i + 1) * page_rows > first || (int64_t)i * page_rows < s.sinks)) return false;
+    return true;
   }
   int pages_for(int64_t rows) const { return (int)((rows + page_rows - 1) / page_rows); }
 };
@@ -101,6 +110,8 @@ int64_t mr_pp_fork(mr_page_pool* pp, int64_t seq, int rows) {
     if (it == pp->seqs.end() || !pp->can_end_at(it->second, rows)) return -(int64_t)MR_ERR_INVALID_ARG;
     Seq s;
     s.rows = rows;
+    s.window = it->second.window;
+    s.sinks = it->second.sinks;
     s.pages.assign(it->second.pages.begin(), it->second.pages.begin() + pp->pages_for(rows));
     const int64_t id = pp->next_id;
     Seq& kept = pp->seqs.emplace(id, std::move(s)).first->second;
@@ -170,6 +181,8 @@ int mr_pp_slide(mr_page_pool* pp, int64_t seq, int window, int sinks) {
       s.pages[i] = -1;
       ++n;
     }
+    s.window = window;
+    s.sinks = sinks;
     return n;
   });
 }

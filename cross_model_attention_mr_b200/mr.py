@@ -904,6 +904,8 @@ class PagePool:
         return [(int(pair[0]), int(pair[1]))] if n else []
 
     def truncate(self, seq: int, rows: int) -> None:
+        """Drop the last rows so that `rows` remain; refused, as a fork is, when `slide` gave up a page that the next
+        query would see then."""
         check(LIB.mr_pp_truncate(self.h, int(seq), int(rows)), "mr_pp_truncate")
 
     def slide(self, seq: int, window: int, sinks: int = 0) -> int:

@@ -598,7 +598,7 @@ void mr_pp_destroy(mr_page_pool* pp);
 /* New empty sequence: its id (>= 0). */
 int64_t mr_pp_open(mr_page_pool* pp);
 
-/* New sequence with the first `rows` rows of `seq`, sharing their pages: its id. */
+/* New sequence with the first `rows` rows of `seq`, sharing their pages: its id.  Refused as mr_pp_truncate is. */
 int64_t mr_pp_fork(mr_page_pool* pp, int64_t seq, int rows);
 
 /*
@@ -608,8 +608,11 @@ int64_t mr_pp_fork(mr_page_pool* pp, int64_t seq, int rows);
  */
 int mr_pp_extend(mr_page_pool* pp, int64_t seq, int rows, int32_t* pair);
 
-/* Drop the last rows of `seq` so that `rows` remain; pages without rows are released.  Refused (as a fork is)
- * when the last row that would remain lies in a page given up by mr_pp_slide. */
+/*
+ * Drop the last rows of `seq` so that `rows` remain; pages without rows are released.  Refused when
+ * mr_pp_slide has given up a page that the next query (its position is `rows` or later) would see under
+ * the window and sinks of the last mr_pp_slide, or the page of the last row that would remain.
+ */
 mr_status mr_pp_truncate(mr_page_pool* pp, int64_t seq, int rows);
 
 /*

@@ -183,3 +183,39 @@ def test_append_with_an_upper_bound_of_the_rows(mr, dt):
     want = mr.kv_append(b, table, lens, k, v, cu_q=cu, rope=r, Q=q)
     assert torch.equal(out[:T].transpose(0, 1), want) and bool((out[T:] == 5.0).all())
     assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
+
+
+# ---------------------------------------------------------------------------------------------- rejected rows
+def test_rejected_rows_behind_a_window_that_has_moved_on(mr):
+    """Drafted rows are appended, attended to and partly rejected, under a window that gives pages up; the tables go to the
+    calls as the pool has them, with -1 for pages that were given up, so a page that is needed after all would show."""
+    from test_gpu_paged_serving import Server
+
+    class Plain(Server):
+        def tables(self, seqs):
+            t, n = self.pool.tables(seqs)
+            return torch.from_numpy(t).cuda(), torch.from_numpy(n).cuda()
+
+    s = Plain(mr, 14, 16, 8, 2, 64, seed=26)
+    window, sinks = 40, 20
+    a = s.pool.open()
+    s.append([a], [100])
+    refused = freed = 0
+    rng = np.random.default_rng(5)
+    for _ in range(30):
+        freed += s.pool.slide(a, window, sinks)
+        held = s.pool.rows(a)
+        q, table, lens, cu = s.append([a], [6])
+        O, lse = mr.paged_attn(s.cache, table, lens, q, cu, window=window, sinks=sinks, return_lse=True, ws=s.ws)
+        s.check(O, lse, q, [a], [6], window, sinks, 2.0 ** -16)
+        with pytest.raises(mr.MRError):
+            s.pool.truncate(a, held - 16)      # a page that the next query would see is gone
+        refused += 1
+        keep = held + int(rng.integers(0, 7))
+        s.pool.truncate(a, keep)
+        s.told[a] = tuple(x[:, :keep] for x in s.told[a])
+        s.decode([a], window, sinks)
+    b = s.pool.fork(a, s.pool.rows(a))
+    s.told[b] = s.told[a]
+    s.decode([a, b], window, sinks)
+    assert refused == 30 and freed >= 5 and -1 in s.pool.tables([a])[0]
