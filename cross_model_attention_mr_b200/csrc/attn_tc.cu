@@ -84,10 +84,18 @@ __device__ __forceinline__ void fail(Smem<D>& s, const AttnParams& p, uint32_t d
   s.abort = 1;
 }
 
+// Whether it holds in all lanes.  A vote alone does not say that the lanes go on together, and each has polled in a loop of
+// its own before it; what follows a wait are instructions that a whole warp has to issue as one.
+__device__ __forceinline__ bool warp_all(bool ok) {
+  ok = __all_sync(0xffffffffu, ok);
+  __syncwarp();
+  return ok;
+}
+
 // mbar_wait by a whole warp for the phase with `n`'s parity: all lanes go on, or none.  All of them wait: a form in which
 // one lane did and the others met it at the vote faulted.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t n, const volatile int* abort, uint64_t ns) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, n & 1, abort, ns));
+  return warp_all(mbar_wait(bar, n & 1, abort, ns));
 }
 
 // Rows of positions first .. last: is there one of the N keys from key0 on that some row does not see?
@@ -121,7 +129,7 @@ __device__ void producer(Smem<D>& s, const AttnParams& p, const Share& sh, const
   while (ok && walk.next(sg)) {
     const Unit& u = sg.u;
     if (segs > 0) ok = mbar_wait_sleep(&s.q_empty, (segs - 1) & 1, &s.abort, p.wait_ns, 64);
-    ok = __all_sync(0xffffffffu, ok);
+    ok = warp_all(ok);
     if (!ok) {
       if (lane == 0) fail(s, p, 0xA01);
       break;
@@ -152,7 +160,7 @@ __device__ void producer(Smem<D>& s, const AttnParams& p, const Share& sh, const
         const uint32_t use = item / kSlots;
         ++item;
         if (use > 0) ok = mbar_wait_sleep(&s.slot_empty[sl], (use - 1) & 1, &s.abort, p.wait_ns, 64);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = warp_all(ok);
         if (!ok) {
           --item;
           if (lane == 0) fail(s, p, 0xA02);
@@ -314,7 +322,7 @@ __device__ void fixer(Smem<D>& s, const AttnParams& p, const Share& sh) {
         const int sl = item % kSlots;
         bool ok = mbar_wait_sleep(&s.slot_full[sl], (item / kSlots) & 1, &s.abort, 2 * p.wait_ns, 64);
         ++item;
-        ok = __all_sync(0xffffffffu, ok);
+        ok = warp_all(ok);
         if (!ok) {
           if (lane == 0) fail(s, p, 0xA21);
           return;
@@ -448,6 +456,7 @@ __device__ __noinline__ void put_back(const AttnParams& p, const Seg& sg, uint32
           const float y = __bfloat162float(v[c + t]);
           if (sees && !isfinite(y)) o[t] = __float_as_uint(fmaf(e, y, __uint_as_float(o[t])));
         }
+        __syncwarp();
         tmem_st32(o_addr + c, o);
         tmem_wait_st();
       }
@@ -656,6 +665,7 @@ __device__ __noinline__ bool softmax_steps(Smem<D>& s, const Steps t, float& ref
         ref = mt;
       }
     }
+    __syncwarp();
     l *= f;
     return true;
   };
