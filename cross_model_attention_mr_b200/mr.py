@@ -204,7 +204,10 @@ class Workspace:
         self.ptr = self.buf.data_ptr() + off
 
     def sync_status(self, stream=None) -> int:
-        return LIB.mr_sync_status(self.ptr, _stream(stream))
+        """Status of the last call on this workspace, after all work on ``stream`` (default: the current stream of the
+        workspace's device, whichever device is current)."""
+        with _on(self.buf, stream):
+            return LIB.mr_sync_status(self.ptr, _stream(None))
 
 
 class Bias:
