@@ -12,6 +12,7 @@ import contextlib
 import ctypes
 import math
 import os
+import threading
 from typing import Optional
 
 import numpy as np
@@ -616,7 +617,9 @@ class BlockManager:
 # ------------------------------------------------------------------------------------------------
 # The receiver's paged key-value cache (MapFlow section 6): rotary positions, appending rows,
 # attention of new rows over the cache, copying pages, and the host-side page pool.
-# These calls run on the device of their tensors, whichever device is current.
+# These calls run on the device of their tensors, whichever device is current.  What they find wrong on the device (pages
+# outside the pool, lengths beyond the table, conflicting pairs) is in the workspace's status: ``ws.sync_status()``, or
+# ``last_status()`` for a call that was given no workspace.
 # ------------------------------------------------------------------------------------------------
 _NO_SWITCH = contextlib.nullcontext()
 
@@ -735,6 +738,24 @@ def _ws_for(ws: Optional[Workspace], nbytes, t: torch.Tensor) -> Workspace:
     return ws
 
 
+_made = threading.local()  # workspace and stream of this thread's last call that made its own
+
+
+def _keep(given: Optional[Workspace], ws: Workspace) -> None:
+    if given is None:
+        _made.last = ws, _stream(None)
+
+
+def last_status(stream=None) -> int:
+    """Device status of this thread's last kv_append, paged_decode, paged_attn or pages_copy that was given no
+    workspace, after all work on ``stream`` (default: the call's own).  That workspace is kept until the next such call."""
+    last = getattr(_made, "last", None)
+    if last is None:
+        raise ValueError("no call without a workspace was made")
+    ws, own = last
+    return ws.sync_status(own if stream is None else stream)
+
+
 def _seqs(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor) -> KvSeqs:
     n = kv_len.shape[0]
     t, l = _ints(table, cache.k, "table", 2), _ints(kv_len, cache.k, "kv_len")
@@ -775,11 +796,12 @@ def kv_append(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, K: torc
         seqs = _seqs(cache, table, kv_len)
         if cu_q is not None and cu_q.shape[0] != seqs.n_seq + 1:
             raise ValueError("cu_q must have n_seq + 1 entries")
-        ws = _ws_for(ws, lambda: 0, cache.k)  # (the status word is all this call needs)
+        given, ws = ws, _ws_for(ws, lambda: 0, cache.k)  # (the status word is all this call needs)
         check(LIB.mr_kv_append(ctypes.byref(cache.c), ctypes.byref(seqs), ctypes.byref(rope.c) if rope else None, q, qo,
                                H_q, ctypes.byref(k), ctypes.byref(v),
                                _ints(cu_q, cache.k, "cu_q") if cu_q is not None else None, total, ws.ptr, ws.nbytes,
                                _stream(None)), "mr_kv_append")
+        _keep(given, ws)
     return q_out
 
 
@@ -813,11 +835,12 @@ def paged_decode(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, Q: t
         if Q.shape[1] != seqs.n_seq or Q.shape[2] != cache.d:
             raise ValueError("Q must be [H_q][n_seq][d]")
         out, lse = _attn_out(Q, out, lse, return_lse)
-        ws = _ws_for(ws, lambda: paged_workspace_bytes(cache, H, seqs.n_seq), cache.k)
+        given, ws = ws, _ws_for(ws, lambda: paged_workspace_bytes(cache, H, seqs.n_seq), cache.k)
         check(LIB.mr_paged_decode(ctypes.byref(cache.c), ctypes.byref(seqs), ctypes.byref(q), H,
                                   1.0 / math.sqrt(cache.d) if scale is None else float(scale), int(window), int(sinks),
                                   ctypes.byref(_rows(out, cache.k, "out")), lse.data_ptr() if lse is not None else None,
                                   ws.ptr, ws.nbytes, _stream(None)), "mr_paged_decode")
+        _keep(given, ws)
     return out if lse is None else (out, lse)
 
 
@@ -836,12 +859,13 @@ def paged_attn(cache: KVCache, table: torch.Tensor, kv_len: torch.Tensor, Q: tor
         if cu_q.shape[0] != seqs.n_seq + 1:
             raise ValueError("cu_q must have n_seq + 1 entries")
         out, lse = _attn_out(Q, out, lse, return_lse)
-        ws = _ws_for(ws, lambda: paged_workspace_bytes(cache, H, seqs.n_seq), cache.k)
+        given, ws = ws, _ws_for(ws, lambda: paged_workspace_bytes(cache, H, seqs.n_seq), cache.k)
         check(LIB.mr_paged_attn(ctypes.byref(cache.c), ctypes.byref(seqs), ctypes.byref(q), H,
                                 _ints(cu_q, cache.k, "cu_q"), total,
                                 1.0 / math.sqrt(cache.d) if scale is None else float(scale), int(window), int(sinks),
                                 ctypes.byref(_rows(out, cache.k, "out")), lse.data_ptr() if lse is not None else None,
                                 ws.ptr, ws.nbytes, _stream(None)), "mr_paged_attn")
+        _keep(given, ws)
     return out if lse is None else (out, lse)
 
 
@@ -864,10 +888,11 @@ def pages_copy(pools, pairs: torch.Tensor, ws: Optional[Workspace] = None, strea
         p = _ints(pairs, first, "pairs", 2)
         if pairs.shape[1] != 2:
             raise ValueError("pairs must be [n][2]")
-        ws = _ws_for(ws, pages_copy_workspace_bytes, first)
+        given, ws = ws, _ws_for(ws, pages_copy_workspace_bytes, first)
         ptrs = (_c_p * len(pools))(*[t.data_ptr() for t in pools])
         check(LIB.mr_pages_copy(ptrs, len(pools), page_bytes, first.shape[0], p, pairs.shape[0], ws.ptr, ws.nbytes,
                                 _stream(None)), "mr_pages_copy")
+        _keep(given, ws)
 
 
 class PagePool:

@@ -219,3 +219,44 @@ def test_rejected_rows_behind_a_window_that_has_moved_on(mr):
     s.told[b] = s.told[a]
     s.decode([a, b], window, sinks)
     assert refused == 30 and freed >= 5 and -1 in s.pool.tables([a])[0]
+
+
+# ---------------------------------------------------------------------------------------------- no workspace given
+def test_status_of_calls_without_a_workspace(mr):
+    import threading
+    c = Case(mr, [1, 20], [40, 20], 2, 1, 16, 64, "bf16", seed=27)
+    cache, table, lens, q = c.args()
+    bad = table.clone()
+    bad[0, 1] = 10 ** 6
+    k, v = rand((1, 2, 64), "bf16", 1), rand((1, 2, 64), "bf16", 2)
+    two = q[:, :2].contiguous()
+    pairs = torch.tensor([[0, 1], [2, 1]], dtype=torch.int32).cuda()
+    calls = [lambda t, **kw: mr.paged_decode(cache, t, lens, two, **kw),
+             lambda t, **kw: mr.paged_attn(cache, t, lens, q, c.cu, **kw),
+             lambda t, **kw: mr.kv_append(cache, t, lens - 10, k, v, **kw),
+             lambda t, **kw: mr.pages_copy([cache.k], pairs if t is bad else pairs[:1], **kw)]
+    st = torch.cuda.Stream()
+    for call in calls:
+        for kw in ({}, {"stream": st}):
+            torch.cuda.synchronize()
+            call(bad, **kw)
+            assert mr.last_status() == mr.MR_ERR_DEVICE_CHECK
+            with pytest.raises((ValueError, TypeError, mr.MRError)):
+                mr.paged_decode(cache, bad, lens, two, window=-1)        # a refused call has no status
+            call(table, ws=c.ws)                                         # nor is one asked for with a workspace of its own
+            assert mr.last_status() == mr.MR_ERR_DEVICE_CHECK
+            torch.cuda.synchronize()
+            call(table, **kw)
+            assert mr.last_status() == mr.MR_OK
+    calls[0](bad)
+    seen = []
+
+    def other():
+        with pytest.raises(ValueError):
+            mr.last_status()
+        calls[0](table)
+        seen.append(mr.last_status())
+    th = threading.Thread(target=other)
+    th.start()
+    th.join()
+    assert seen == [mr.MR_OK] and mr.last_status() == mr.MR_ERR_DEVICE_CHECK
