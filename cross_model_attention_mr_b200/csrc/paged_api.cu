@@ -80,6 +80,9 @@ bool rope_ok(const mr_rope* r) {
          r->rot_dim % 2 == 0 && isfinite(r->mscale);
 }
 
+// the kernels work in base 2: scale * log2(e) has to be finite, too
+bool scale_ok(float scale) { return isfinite(scale * 1.4426950408889634f); }
+
 // the status word in front of a workspace, cleared in stream order
 cudaError_t reset_header(void* ws, cudaStream_t st) { return cudaMemsetAsync(ws, 0, sizeof(WsHeader), st); }
 
@@ -156,7 +159,7 @@ mr_status mr_paged_decode(const mr_kv_cache* cache, const mr_kv_seqs* seqs, cons
                           size_t ws_bytes, void* stream) {
   mr_status e;
   if ((e = cache_ok(cache)) != MR_OK || (e = pools_ok(cache)) != MR_OK || (e = seqs_ok(seqs)) != MR_OK) return e;
-  if (H_q < 1 || H_q % cache->H_kv || window < 0 || sinks < 0 || !isfinite(scale)) return MR_ERR_INVALID_ARG;
+  if (H_q < 1 || H_q % cache->H_kv || window < 0 || sinks < 0 || !scale_ok(scale)) return MR_ERR_INVALID_ARG;
   if (H_q > kMaxHeads) return MR_ERR_UNSUPPORTED;
   const int es = esize(cache->dt), d = cache->d;
   if (!rows_ok(Q, H_q, seqs->n_seq, d, es, false) || !rows_ok(O, H_q, seqs->n_seq, d, es, true))
@@ -186,7 +189,7 @@ mr_status mr_paged_attn(const mr_kv_cache* cache, const mr_kv_seqs* seqs, const 
                         const mr_rows* O, float* lse, void* ws, size_t ws_bytes, void* stream) {
   mr_status e;
   if ((e = cache_ok(cache)) != MR_OK || (e = pools_ok(cache)) != MR_OK || (e = seqs_ok(seqs)) != MR_OK) return e;
-  if (H_q < 1 || H_q % cache->H_kv || window < 0 || sinks < 0 || !isfinite(scale)) return MR_ERR_INVALID_ARG;
+  if (H_q < 1 || H_q % cache->H_kv || window < 0 || sinks < 0 || !scale_ok(scale)) return MR_ERR_INVALID_ARG;
   if (H_q > kMaxHeads) return MR_ERR_UNSUPPORTED;
   if (!aligned(cu_q, 4) || total_q < 0) return MR_ERR_INVALID_ARG;
   const int es = esize(cache->dt), d = cache->d;

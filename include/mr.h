@@ -539,6 +539,7 @@ mr_status mr_kv_append(const mr_kv_cache* cache, const mr_kv_seqs* seqs, const m
  *   O_h = sum_j softmax_j(scale * q_h.k_j) v_j over the rows j visible from position kv_len[s] - 1,
  * query head h reading key-value head h / (H_q / H_kv).  Q, O: H_q heads, row s for sequence s.
  *   lse  NULL or device fp32 [H_q][n_seq]: natural log of sum_j exp(scale * q.k_j)
+ *   scale  finite, and so that scale * log2(e) is (up to 2.3e38 in magnitude)
  * A sequence without visible rows gets O = 0 and lse = -inf.  Rows that are not visible, stale rows of
  * the last page among them, do not influence the result whatever they hold (infinities and NaN too).
  * H_q must be a multiple of H_kv.  Work is split along every sequence's length over the whole GPU

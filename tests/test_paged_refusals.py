@@ -1,5 +1,5 @@
-"""Addresses that the paged cache's kernels could not read or write in whole elements are refused on the host, before
-anything is launched.  No GPU is needed: a refused call touches no device."""
+"""Addresses that the paged cache's kernels could not read or write in whole elements, and scales that they could not work
+with, are refused on the host, before anything is launched.  No GPU is needed: a refused call touches no device."""
 import ctypes
 
 import pytest
@@ -28,12 +28,12 @@ def _calls(mr):
         return mr.LIB.mr_kv_append(_ref(cache), _ref(mr.KvSeqs(table, kv_len, 4, 3)), _ref(rope.c), _ref(x), _ref(x), 4,
                                    _ref(x), _ref(x), cu, 10, ws, n_ws, None)
 
-    def decode(table=FAKE, kv_len=FAKE, lse=None, ws=FAKE):
-        return mr.LIB.mr_paged_decode(_ref(cache), _ref(mr.KvSeqs(table, kv_len, 4, 3)), _ref(x), 4, 0.125, 0, 0, _ref(x),
+    def decode(table=FAKE, kv_len=FAKE, lse=None, ws=FAKE, scale=0.125):
+        return mr.LIB.mr_paged_decode(_ref(cache), _ref(mr.KvSeqs(table, kv_len, 4, 3)), _ref(x), 4, scale, 0, 0, _ref(x),
                                       lse, ws, n_ws, None)
 
-    def attn(table=FAKE, kv_len=FAKE, cu=FAKE, lse=None, ws=FAKE):
-        return mr.LIB.mr_paged_attn(_ref(cache), _ref(mr.KvSeqs(table, kv_len, 4, 3)), _ref(x), 4, cu, 10, 0.125, 0, 0,
+    def attn(table=FAKE, kv_len=FAKE, cu=FAKE, lse=None, ws=FAKE, scale=0.125):
+        return mr.LIB.mr_paged_attn(_ref(cache), _ref(mr.KvSeqs(table, kv_len, 4, 3)), _ref(x), 4, cu, 10, scale, 0, 0,
                                     _ref(x), lse, ws, n_ws, None)
 
     def copy(pairs=FAKE, ws=FAKE):
@@ -52,3 +52,10 @@ def test_misaligned_addresses_are_refused(mr, name, what):
     call = _calls(mr)[name]
     for off in (1, 2, 3) + ((4, 8, 12) if what == "ws" else ()):
         assert call(**{what: FAKE + off}) == mr.MR_ERR_INVALID_ARG, off
+
+
+@pytest.mark.parametrize("name", ["decode", "attn"])
+@pytest.mark.parametrize("scale", [3e38, -3e38, 2.4e38])
+def test_scales_that_overflow_in_base_2_are_refused(mr, name, scale):
+    """They would make products of infinity and 0 of every score that is 0."""
+    assert _calls(mr)[name](scale=scale) == mr.MR_ERR_INVALID_ARG
