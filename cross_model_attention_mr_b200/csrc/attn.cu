@@ -106,11 +106,12 @@ __device__ __forceinline__ void store4(const AttnParams& p, int64_t at, float4 x
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 2) k_attn(const AttnParams p) {
+__global__ void __launch_bounds__(kThreads, 2) k_attn(const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem<D>& s = *reinterpret_cast<Smem<D>*>(smem_raw);
   constexpr int kStride = Smem<D>::kStride, kPStride = Smem<D>::kPStride;
   constexpr int kSlot = kRows * (D + 2);  // floats of a part: 64 (maximum, sum), then outputs
+  if (p.few.ask && as_tokens<kThreads>(p.kv, p.cu, p.total_q, p.window, p.sinks, p.few, s.part.sums)) return;
   empty_rows<T, D, kThreads>(p);
   Share sh;
   if (!make_share<kKeys, kThreads>(p, s.part, sh)) return;
@@ -350,6 +351,30 @@ cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
 
 constexpr size_t kCounterBytes = (kAttnMaxCtas * sizeof(uint32_t) + 255) / 256 * 256;
 
+// Few rows: each as a token of its own (ask 0), in tiles (-1), or as the lengths on the device say (1).  A row of its own
+// reads its keys and values again, from L2 mostly, but no tile of query rows stands nearly empty, and P keeps its second
+// part.  What decides is how much is read again, and that depends on how the rows are spread over the sequences, which the
+// host does not know: 256 sequences of 1000 with one row each take 172 us as tokens and 333 in tiles, 256 of 4096 with all
+// rows in one of them 391 and 141.  So where the host's bound leaves it open both kernels are launched, and one of them
+// leaves at once (3 to 9 us more); calls of more than `most` rows, and more than sequences, run in tiles.  Measured, tokens
+// / tiles in us, heads of 128:
+//   bf16: up to 256 MB more.  32 heads in groups of 4: 1 sequence of 4096 with 8, 16 and 32 rows 27/33, 39/45 and 62/34; of
+//   16384 with 2, 4 and 8 27/33, 39/39 and 62/47; 8 of 4096 with 1, 2 and 4 each 36/48, 51/47 and 85/49.  Groups of 1: 1 of
+//   4096 with 2, 4 and 8 27/29, 39/31 and 62/36.
+//   fp32: that, or 8 times as much, since the tiles are bound by their arithmetic.  1 of 65536 with 4, 8 and 16: 351/747,
+//   683/747 and 1347/748; in groups of 8 431/747 and 841/749; 8 of 4096 with 1, 4 and 8 each: 63/271, 192/273 and 358/273.
+FewRows few_rows(const AttnArgs& a) {
+  const int n_seq = a.kv.n_seq;
+  const int most = a.dt == MR_BF16 ? 16 : n_seq <= 2 ? 8 : n_seq < 16 ? 4 * n_seq : 64;
+  if (a.total_q <= 0 || a.total_q > (most > n_seq ? most : n_seq)) return FewRows{-1, 0, 0};
+  const int64_t key_bytes = (int64_t)a.kv.H_kv * a.kv.d * 2 * (a.dt == MR_BF16 ? 2 : 4);
+  FewRows f{1, ((int64_t)256 << 20) / key_bytes, a.dt == MR_BF16 ? 1 : 8};
+  int64_t seen = a.kv.capacity;  // keys that a row sees at most
+  if (a.window > 0 && (int64_t)a.window + a.sinks < seen) seen = (int64_t)a.window + a.sinks;
+  if (a.total_q <= f.times || (a.total_q - 1) * seen <= f.extra) f.ask = 0;
+  return f;
+}
+
 }  // namespace
 
 size_t attn_workspace_bytes(mr_dtype dt, int d) {
@@ -368,14 +393,8 @@ void attn_split(AttnParams& p, int rows, int max_heads) {
 cudaError_t launch_attn(const AttnArgs& a) {
   int dev = 0, sms = 0;
   cudaError_t e;
-  // Few rows: each as a token of its own.  Every row then reads its keys and values again, from L2 mostly, but no tile of
-  // query rows stands nearly empty, and P keeps its second part.  32 heads in groups of 4, this way against tiles: bf16,
-  // 1 sequence of 200 rows, 8 of them new: 11 and 23 us; of 4096, 16 new: 38 and 45; 8 sequences of 4096 with 1, 2 and 4
-  // new rows each: 35 and 48, 51 and 48, 84 and 49.  fp32, 1 of 4096 with 8 and 16: 60 and 80, 100 and 82; 8 of 4096
-  // with 1, 4 and 8 each: 65 and 281, 195 and 283, 364 and 283.
-  const int n_seq = a.kv.n_seq;
-  const int few = a.dt == MR_BF16 ? 16 : n_seq <= 2 ? 8 : n_seq < 16 ? 4 * n_seq : 64;
-  if (a.total_q > 0 && a.total_q <= (few > n_seq ? few : n_seq)) {
+  const FewRows few = few_rows(a);
+  if (few.ask >= 0) {
     DecodeArgs d;
     d.kv = a.kv;
     d.cu_q = a.cu_q;
@@ -389,14 +408,17 @@ cudaError_t launch_attn(const AttnArgs& a) {
     d.sinks = a.sinks;
     d.lse = a.lse;
     d.ws = a.ws;
+    d.few = few;
     d.stream = a.stream;
-    return launch_decode(d);
+    if ((e = launch_decode(d)) != cudaSuccess || !few.ask) return e;
   }
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  if ((e = cudaMemsetAsync(a.ws, 0, kWsHeaderBytes + kCounterBytes, a.stream)) != cudaSuccess) return e;
+  // (behind the tokens' kernel the counters are zero: only one of the two uses them)
+  if (few.ask < 0 && (e = cudaMemsetAsync(a.ws, 0, kWsHeaderBytes + kCounterBytes, a.stream)) != cudaSuccess) return e;
   if (a.total_q == 0) return cudaSuccess;
   AttnParams p{};
+  p.few = FewRows{few.ask > 0, few.extra, few.times};
   p.kv = a.kv;
   p.q = a.q.ptr;
   p.o = a.o.ptr;

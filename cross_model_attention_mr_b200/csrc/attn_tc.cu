@@ -863,6 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     set_status(p.ws, MR_ERR_DEVICE_CHECK, 0xA41);
     return;
   }
+  if (p.few.ask && as_tokens<kThreads>(p.kv, p.cu, p.total_q, p.window, p.sinks, p.few, s.part.sums)) return;
   empty_rows<__nv_bfloat16, D, kThreads>(p);
   Share sh;
   if (!make_share<kKeys, kThreads>(p, s.part, sh)) return;  // nothing for this CTA (all its threads leave)

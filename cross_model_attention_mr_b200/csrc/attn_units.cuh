@@ -33,6 +33,7 @@ struct AttnParams {
   uint32_t* counters;                    // one per CTA, zero at launch
   float* part;                           // two slots per CTA
   uint64_t wait_ns;                      // (tensor-core kernel) limit of its waits
+  FewRows few;
   int skip_arrive;                       // failure-path test: tile A's softmax keeps its first P back
 };
 

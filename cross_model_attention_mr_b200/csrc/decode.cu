@@ -55,6 +55,7 @@ struct Params {
   int vec_q, vec_o;                      // rows aligned to 4 (Q) and 16 (O) bytes
   float a;                               // scale * log2(e)
   int window, sinks;
+  FewRows few;
   WsHeader* ws;
   uint32_t* counters;                    // [kMaxCtas], zero at launch
   float* part;                           // [2 * kMaxCtas][kMaxRows * (d + 2)]
@@ -600,9 +601,10 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) k_decode(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ int sh_row, sh_last;
-  __shared__ int64_t sh_sum[kWarps], sh_before;
+  __shared__ int64_t sh_sum[2 * kWarps], sh_before;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_rows = p.n_rows;
+  if (p.few.ask && !as_tokens<kThreads>(p.kv, p.cu, n_rows, p.window, p.sinks, p.few, sh_sum)) return;
   // tiles in front of this thread's run of query rows
   const int per = (n_rows + kThreads - 1) / kThreads;
   const int t_lo = min(n_rows, (int)threadIdx.x * per), t_hi = min(n_rows, t_lo + per);
@@ -767,6 +769,7 @@ cudaError_t launch_decode(const DecodeArgs& a) {
   p.a = a.scale * kLog2e;
   p.window = a.window;
   p.sinks = a.sinks;
+  p.few = a.few;
   p.ws = (WsHeader*)a.ws;
   p.counters = (uint32_t*)((char*)a.ws + kWsHeaderBytes);
   p.part = (float*)((char*)a.ws + kWsHeaderBytes + kCounterBytes);

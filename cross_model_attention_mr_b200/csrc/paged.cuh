@@ -23,6 +23,41 @@ __device__ __forceinline__ int pool_row(const PagedKv& kv, int s, int g, int j) 
   return (page * kv.H_kv + g) * kv.page_rows + (j - pi * kv.page_rows);
 }
 
+// Whether the new rows are worked on as tokens of their own.  Every CTA of both kernels comes to the same answer.  Whole CTA
+// of NT threads; sums: shared memory for 2 * NT / 32 values.
+template <int NT>
+__device__ __noinline__ bool as_tokens(const PagedKv& kv, const int32_t* cu, int total_q, int window, int sinks,
+                                       const FewRows& few, int64_t* sums) {
+  int64_t once = 0, all = 0;  // keys that the sequences' last rows see; times their new rows
+  for (int s = threadIdx.x; s < kv.n_seq; s += NT) {
+    const int q0 = min(max(__ldg(cu + s), 0), total_q);
+    const int n = min(max(__ldg(cu + s + 1), q0), total_q) - q0;
+    if (n == 0) continue;
+    const int len = max(__ldg(kv.kv_len + s), 0), held = min(len, kv.capacity);
+    const int lo = window > 0 ? min(max(len - window, 0), held) : 0;
+    const int64_t seen = min(sinks, lo) + (held - lo);
+    once += seen;
+    all += seen * n;
+  }
+#pragma unroll
+  for (int w = 16; w; w >>= 1) {
+    once += __shfl_xor_sync(0xffffffffu, once, w);
+    all += __shfl_xor_sync(0xffffffffu, all, w);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    sums[threadIdx.x >> 5] = once;
+    sums[NT / 32 + (threadIdx.x >> 5)] = all;
+  }
+  __syncthreads();
+  once = all = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    once += sums[w];
+    all += sums[NT / 32 + w];
+  }
+  __syncthreads();  // the sums' place is free again
+  return all - once <= few.extra || all <= few.times * once;
+}
+
 // Mask of the bf16 halves of w that are infinite or NaN (an exponent of all ones carries into the bit above when one is
 // added to it).
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {

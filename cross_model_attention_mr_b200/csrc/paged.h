@@ -30,6 +30,13 @@ struct PagedKv {
   FastDiv by_rows;
 };
 
+// New rows of a chunk as tokens of their own (decode.cu) or in tiles (attn.cu, attn_tc.cu), decided on the device: as
+// tokens where at most `extra` keys are read more often than once for each sequence, or `times` as many in all.
+struct FewRows {
+  int ask;  // 0: decided already
+  int64_t extra, times;
+};
+
 struct AppendArgs {
   PagedKv kv;
   const mr_rope* rope;  // host; NULL = no rotation
@@ -63,6 +70,7 @@ struct DecodeArgs {
   int window, sinks;
   float* lse;
   void* ws;  // decode_workspace_bytes: status header, join counters, partial results
+  FewRows few;
   cudaStream_t stream;
 };
 

@@ -180,6 +180,7 @@ mr_status mr_paged_decode(const mr_kv_cache* cache, const mr_kv_seqs* seqs, cons
   a.sinks = sinks;
   a.lse = lse;
   a.ws = ws;
+  a.few = FewRows{};
   a.stream = (cudaStream_t)stream;
   return from_cuda(launch_decode(a));
 }

@@ -260,3 +260,70 @@ def test_status_of_calls_without_a_workspace(mr):
     th.start()
     th.join()
     assert seen == [mr.MR_OK] and mr.last_status() == mr.MR_ERR_DEVICE_CHECK
+
+
+# ---------------------------------------------------------------------------------------------- tokens or tiles
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("spread", ["one each", "all in one", "some"])
+def test_few_rows_however_they_are_spread(mr, dt, spread):
+    """Batches whose rows' way through the library depends on the lengths on the device (pages are shared between the
+    sequences, so that they can be long)."""
+    n, pr, d, Hq, Hk, long = 96, 64, 128, 4, 2, 7000
+    new = {"one each": [1] * n, "all in one": [0] * 40 + [n] + [0] * (n - 41), "some": [2, 0, 0, 0, 5, 1] * 16}[spread]
+    held = [long if i % 3 == 1 else 65 + 7 * i for i in range(n)]
+    pages = -(-long // pr)
+    k, v = rand((pages, Hk, pr, d), dt, 31), rand((pages, Hk, pr, d), dt, 32)
+    cache = mr.KVCache(k, v)
+    # (wide tables: the host's bound is the table, not the lengths)
+    table = torch.zeros((n, 4 * pages), dtype=torch.int32)
+    table[:, :pages] = torch.stack([torch.randperm(pages, generator=torch.Generator().manual_seed(i)) for i in range(n)])
+    lens = torch.tensor(held, dtype=torch.int32)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32).cuda()
+    q = rand((Hq, sum(new), d), dt, 33)
+    ws = mr.Workspace(mr.paged_workspace_bytes(cache, Hq, n))
+    O, lse = mr.paged_attn(cache, table.cuda(), lens.cuda(), q, cu, return_lse=True, ws=ws)
+    assert ws.sync_status() == mr.MR_OK
+    want, wl, A, S = attend(np64(q), np64(k), np64(v), table.numpy(), held, new, float(np.float32(1 / math.sqrt(d))))
+    tol, ltol = attend_tol(want, wl, A, S, d, long, torch.finfo(DT[dt]).eps, ATTN_P[dt])
+    assert np.all(np.abs(np64(O) - want) <= tol) and np.all(np.abs(np64(lse) - wl) <= ltol)
+
+
+def test_how_rows_are_spread_decides(mr):
+    """With the test hook the tensor-core kernel's tiles run into their time limit, so the status tells which way a call
+    took: rows of their own where each sequence has one, tiles where one sequence has them all, also when a captured call
+    meets other lengths and offsets."""
+    n, pr, Hk, d, long = 64, 128, 4, 128, 20000
+    cache = mr.KVCache(*(rand((-(-long // pr), Hk, pr, d), "bf16", 34 + i) for i in range(2)))
+    table = torch.arange(-(-long // pr), dtype=torch.int32).expand(n, -1).contiguous().cuda()
+    lens = torch.full((n,), long, dtype=torch.int32).cuda()
+    offsets = lambda new: torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32).cuda()
+    each, one = offsets([1] * n), offsets([0] * 7 + [n] + [0] * (n - 8))
+    q = rand((8, n, d), "bf16", 36)
+    ws = mr.Workspace(mr.paged_workspace_bytes(cache, 8, n))
+    plain = {}
+    for name, cu in (("each", each), ("one", one)):
+        plain[name] = mr.paged_attn(cache, table, lens, q, cu, ws=ws)
+        assert ws.sync_status() == mr.MR_OK
+    assert torch.equal(plain["each"], mr.paged_decode(cache, table, lens, q))
+    cu, out = each.clone(), torch.zeros_like(q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mr.paged_attn(cache, table, lens, q, cu, out=out, ws=ws)
+    for name, to in (("one", one), ("each", each), ("one", one)):
+        cu.copy_(to)
+        g.replay()
+        assert ws.sync_status() == mr.MR_OK and torch.equal(out, plain[name])
+    assert mr.LIB.mr_debug_set(1_000_000, 1) == mr.MR_OK
+    try:
+        for to, want in ((each, mr.MR_OK), (one, mr.MR_ERR_TIMEOUT)):
+            mr.paged_attn(cache, table, lens, q, to, ws=ws)
+            assert ws.sync_status() == want
+        lens.fill_(200)                              # little is read again: rows of their own either way
+        mr.paged_attn(cache, table, lens, q, one, ws=ws)
+        assert ws.sync_status() == mr.MR_OK
+        # a short table is recorded whichever way is taken
+        lens.fill_(long + 5000)
+        mr.paged_attn(cache, table, lens, q, each, ws=ws)
+        assert ws.sync_status() == mr.MR_ERR_DEVICE_CHECK
+    finally:
+        assert mr.LIB.mr_debug_set(0, 0) == mr.MR_OK
