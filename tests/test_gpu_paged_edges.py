@@ -327,3 +327,76 @@ def test_how_rows_are_spread_decides(mr):
         assert ws.sync_status() == mr.MR_ERR_DEVICE_CHECK
     finally:
         assert mr.LIB.mr_debug_set(0, 0) == mr.MR_OK
+
+
+# ---------------------------------------------------------------------------------------------- many pairs, bf16 gradients
+def test_page_copies_of_more_pairs_than_threads(mr):
+    """Conflicts between pairs that the same thread of a block looks at, one round after the other."""
+    n, most = 4000, 1500
+    pool = torch.arange(n * 64, dtype=torch.float32, device="cuda").view(n, 1, 1, 64).contiguous()
+    order = torch.randperm(n, generator=torch.Generator().manual_seed(3)).to(torch.int32)
+    pairs = torch.stack([order[:most], order[most: 2 * most]], 1)
+    ws = mr.Workspace(mr.pages_copy_workspace_bytes())
+    old = pool.clone()
+    mr.pages_copy([pool], pairs.cuda(), ws=ws)
+    assert ws.sync_status() == mr.MR_OK
+    want = old.clone()
+    want[pairs[:, 1].long()] = old[pairs[:, 0].long()]
+    assert torch.equal(pool, want)
+    # far apart in the list: a destination named twice (the first counts), sources that others write, a swap, pages that
+    # do not exist, and a page with itself, which counts for nothing
+    bad = pairs.clone()
+    bad[1400, 1] = bad[3, 1]                     # 1400 is skipped
+    bad[700, 0] = bad[1301, 1]                   # 700 is skipped
+    bad[20] = torch.tensor([int(bad[1290, 1]), int(bad[1290, 0])])  # 20 and 1290 would swap: both are skipped
+    bad[900, 0], bad[901, 1] = n, -1             # 900 and 901 are skipped
+    bad[1450, 0] = bad[1450, 1]
+    pool.copy_(old)
+    mr.pages_copy([pool], bad.cuda(), ws=ws)
+    assert ws.sync_status() == mr.MR_ERR_DEVICE_CHECK
+    want = old.clone()
+    keep = [i for i in range(most) if i not in (1400, 700, 20, 1290, 900, 901, 1450)]
+    want[bad[keep, 1].long()] = old[bad[keep, 0].long()]
+    assert torch.equal(pool, want)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("scaling", ["none", "ramp"])
+def test_adjoint_of_the_rotation_in_bf16(mr, interleaved, scaling):
+    """The formula in 64 bits, and differences of the forward call: the rotation is linear, so a difference over a whole
+    unit has no other error than the forward's rounding."""
+    from paged_ref import inv_freq
+    from test_gpu_paged_rope import check_rotated
+    H, T, d, rot = 3, 50, 128, 96
+    kw = dict(scaling=scaling, factor=4.0 if scaling == "ramp" else 1.0)
+    g = rand((H, T, d), "bf16", 41)
+    pos = torch.randint(0, 100000, (T,), generator=torch.Generator().manual_seed(42), dtype=torch.int32)
+    r = mr.Rope(d, rot_dim=rot, interleaved=interleaved, orig_len=4096, mscale=1.125, **kw)
+    gx = mr.rope(r, g, pos.cuda(), adjoint=True)
+    check_rotated(gx, g, pos.numpy(), inv_freq(rot, **kw), "bf16", interleaved, 1.125, -1)
+    step = torch.zeros((d, T, d), dtype=torch.bfloat16, device="cuda")
+    step[torch.arange(d), :, torch.arange(d)] = 1.0      # head e: a unit of element e in every row
+    diff = np64(mr.rope(r, step, pos.cuda()))            # [e][row][element]
+    for h in range(H):
+        want = np.einsum("etc,tc->te", diff, np64(g)[h])
+        # two elements of a column are not zero, each off by half a step (2^-8 of at most 1.125) and 2^-21 for the
+        # rotation; gx itself is rounded once
+        tol = (2.0 ** -8 + 2.0 ** -20) * 1.125 * 2 * np.abs(np64(g)[h]).max(1, keepdims=True) + 2.0 ** -8 * np.abs(want)
+        assert np.all(np.abs(want - np64(gx)[h]) <= tol)
+
+
+# ---------------------------------------------------------------------------------------------- the queries' own place
+@pytest.mark.parametrize("dt,pr", [("bf16", 16), ("bf16", 12), ("f32", 16)])
+@pytest.mark.parametrize("new,held", [([1, 1, 1], [9000, 40, 3]), ([200, 3, 90], [3000, 3, 500]), ([5, 2], [700, 2])])
+def test_outputs_in_the_queries_place(mr, dt, pr, new, held):
+    c = Case(mr, new, held, 8, 2, pr, 128, dt, seed=43)
+    cache, table, lens, q = c.args()
+    want = mr.paged_attn(cache, table, lens, q, c.cu, ws=c.ws)
+    got = q.clone()
+    mr.paged_attn(cache, table, lens, got, c.cu, out=got, ws=c.ws)
+    assert torch.equal(got, want)
+    if max(new) == 1:
+        want = mr.paged_decode(cache, table, lens, q, ws=c.ws)
+        got = q.clone()
+        mr.paged_decode(cache, table, lens, got, out=got, ws=c.ws)
+        assert torch.equal(got, want)
