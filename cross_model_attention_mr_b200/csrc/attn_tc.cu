@@ -12,13 +12,16 @@
 //     softmax works on one half while the products that the other half waits for run.  S, P and O of a tile are ordered
 //     by the tensor core's own order, so no barrier says that P has been read;
 //   * two softmax warpgroups, a query row per thread: the mask only where some row does not see some key, a row reference
-//     that moves when a score passes it by 2^8 (O is then rescaled in Tensor Memory), P = 2^(x - reference) in bf16;
+//     that moves when a score passes it by 2^8 (O is then rescaled in Tensor Memory), P = 2^(x - reference) rounded to bf16
+//     once, the type that its product with V takes (off by at most 2^-8 of itself, as V is; the sums are of P before that.
+//     A second part for what is rounded off, as in decoding, would be half as many products again);
 //   * a fix-up warp looks after the values of key tiles that not every row sees: rows that nobody of the unit sees become
 //     zeros (0 * NaN would not be 0); in rows that only some see, values that are not finite do, and the softmax warps
 //     add them at the end to the rows that do see them.
 // Bound by the chain S -> softmax -> P V -> S of each tile, two of which overlap: 16384 exponentials per tile at 16 a
 // clock take as long as its two products, and neither alone fills the time.  4 suffixes of 512 to 2048 rows behind 4096,
-// 32 heads of 128: 375 us, 1.09 PFLOP/s, the tensor pipe 67% busy (52% its math, the rest operands from shared memory).
+// 32 heads of 128: 377 us replayed from a graph, 1.08 PFLOP/s, the tensor pipe 68% busy (53% its math, the rest operands
+// from shared memory); 439 us as a call among others, under the power limit.  Heads of 64, pages of 16 rows: 295 us.
 // Every wait is bounded (MR_ERR_TIMEOUT, then drain and free Tensor Memory).
 #include <cuda_bf16.h>
 

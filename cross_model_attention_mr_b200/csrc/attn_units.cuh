@@ -3,9 +3,10 @@
 // A unit is (sequence, run of `tokens` new rows, kv head, chunk of `hp` query heads of its group); it reads a list of
 // key tiles of KT rows: the tiles that hold first rows kept visible, then those from the first window's start to the
 // last row's position.  All units' tiles, laid end to end (a run's heads next to one another, each with a few steps for
-// beginning and ending it), are one range of steps that is split evenly over the CTAs: ragged batches, causal and windowed masks, and one long sequence with few new
-// rows load the GPU alike.  A CTA's share may begin and end inside a unit; such parts are joined through the workspace
-// by the CTA that finishes last, in the order of the keys.  No CTA waits for another one.
+// beginning and ending it), are one range of steps that is split evenly over the CTAs: ragged batches, causal and windowed
+// masks, and one long sequence with few new rows load the GPU alike.  A CTA's share may begin and end inside a unit; such
+// parts are joined through the workspace by the CTA that finishes last, in the order of the keys.  No CTA waits for
+// another one.
 #pragma once
 
 #include "paged.cuh"
@@ -27,8 +28,9 @@ struct AttnParams {
   int negate;                            // the scores' sign is changed (tensor-core kernel: a stays positive)
   int window, sinks;
   int unit_cost;                         // steps that beginning and ending a unit take
-  int min_steps;                         // a CTA's share is at least this ...
-  int max_parts;                         // ... and no unit has many more parts than this
+  // As many CTAs take part as leave each a share of about min_steps, or of about the longest unit's steps / max_parts if
+  // that is more (rounding may halve a share, and so double a unit's parts).
+  int min_steps, max_parts;
   WsHeader* ws;
   uint32_t* counters;                    // one per CTA, zero at launch
   float* part;                           // two slots per CTA

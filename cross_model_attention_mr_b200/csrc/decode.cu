@@ -20,8 +20,8 @@
 // instruction (rows 0-7 and 8-15).  A remainder may be 0 or negative, so an infinite value must not meet it: a warp
 // whose sums come out infinite or NaN reads its rows a second time and leaves such values out of that product.  fp32
 // runs on the CUDA cores.
-// 8 sequences of 32768 rows, 64 heads in groups of 8 (1.07 GB): 173 us, 6.2 TB/s, 94% of a copy's rate; 16 sequences of
-// 4608 to 6144 rows, 32 heads in groups of 4: 63 us, 5.6 TB/s.
+// 8 sequences of 32768 rows, 64 heads in groups of 8 (1.07 GB): 177 to 182 us over several machines, 5.9 to 6.1 TB/s, 90 to
+// 93% of a copy's rate; 16 sequences of 4608 to 6144 rows, 32 heads in groups of 4: 65 us, 5.4 TB/s.
 #include <cuda_bf16.h>
 
 #include "paged.cuh"
@@ -68,8 +68,8 @@ struct Cfg {
   static constexpr int kRowsPerCopy = 32 / kChunks;            // rows a warp-wide copy covers
   static constexpr int kCopies = kSlice / kRowsPerCopy;
   static constexpr int kSliceBytes = 2 * kSlice * kRowBytes;   // K and V
-  // about 12 KB in flight for each warp of the SM
-  static constexpr int kStages = sizeof(T) == 4 && D == 128 ? 3 : (sizeof(T) == 2 && D == 64 ? 5 : 3);
+  // slices on the way while one is worked on: 16 KB a warp (fp32 rows of 128: 32 KB)
+  static constexpr int kStages = sizeof(T) == 2 && D == 64 ? 5 : 3;
   static constexpr int kRingBytes = kWarps * kStages * kSliceBytes;
 };
 

@@ -3,7 +3,9 @@
 // Bound by memory: a page is read and written once.  A block moves a chunk of one page of one pool with
 // 16-byte loads, kUnroll in flight per thread.  Whether a pair may be copied depends on all the others (the
 // copies count as simultaneous), so each block compares its pair with the whole list first: at a few
-// thousand pairs that is 32 KB out of L2 per chunk of up to 64 KB, and needs no second launch and no memory.
+// thousand pairs that is 32 KB out of L2 per chunk of up to 64 KB, and needs no second launch and no memory.  It
+// grows with the square of the list: 10000 pairs of 32 KB take 118 us (100 for the copies alone), of 2 KB 83 us (6),
+// 50000 of 2 KB 1.8 ms (31).
 #include "paged.cuh"
 #include "profile.h"
 

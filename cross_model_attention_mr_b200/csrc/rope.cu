@@ -10,9 +10,10 @@
 // instructions a pair), so a thread keeps one unit of a token, two 16-byte vectors, for several heads: the two halves of
 // 8 (fp32: 4) pairs in the half layout, or neighbouring vectors in the interleaved one.  Its loads do not depend on the
 // position, so they are under way while the position is looked up and the sines are computed; nothing is shared between
-// threads.  32 heads x 4096 rows of 128 in bf16: 10.9 us, 6.2 TB/s (a table of sines in shared memory, with the loads
-// behind it, took 36 us); appending 8192 rows of 28 + 2 x 4 heads: 33 us, 4.6 TB/s, as much as the same copies without
-// the sines.
+// threads.  32 heads x 65536 rows of 128 in bf16 (1.07 GB): 168 us, 6.4 TB/s.  4096 rows: 11 to 13 us over several machines
+// with the input in L2 from the call before (5.3 to 6.1 TB/s; a table of sines in shared memory, with the loads behind it,
+// took 36 us), 15.4 us, 4.35 TB/s, with inputs that are not.  Appending 8192 rows of 28 + 2 x 4 heads: 35 us, 4.3 TB/s, from
+// L2 or not.
 #include <cuda_bf16.h>
 
 #include "paged.cuh"

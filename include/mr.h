@@ -542,7 +542,7 @@ mr_status mr_kv_append(const mr_kv_cache* cache, const mr_kv_seqs* seqs, const m
  *   scale  finite, and so that scale * log2(e) is (up to 2.3e38 in magnitude)
  * A sequence without visible rows gets O = 0 and lse = -inf.  Rows that are not visible, stale rows of
  * the last page among them, do not influence the result whatever they hold (infinities and NaN too).
- * H_q must be a multiple of H_kv.  Work is split along every sequence's length over the whole GPU
+ * H_q must be a multiple of H_kv.  O may be Q (the same tensor).  Work is split along every sequence's length over the whole GPU
  * and joined in a fixed order: results do not vary from call to call.
  */
 mr_status mr_paged_decode(const mr_kv_cache* cache, const mr_kv_seqs* seqs, const mr_rows* Q, int H_q,
@@ -558,7 +558,14 @@ mr_status mr_paged_decode(const mr_kv_cache* cache, const mr_kv_seqs* seqs, cons
  * A row that sees nothing (a negative position) gets O = 0 and lse = -inf.  Rows of the cache that a new
  * row does not see do not influence its result, whatever they hold.  Probabilities enter the second
  * product in the cache's type (bf16: off by at most 2^-8 of themselves; calls of few rows, which run as
- * mr_paged_decode does: 2^-16); sums are fp32.
+ * mr_paged_decode does: 2^-16); sums are fp32.  Scores are expected below 2^30 in magnitude.
+ * Few rows (bf16: up to 16, fp32: up to 8, or 4 a sequence and 64 in all; in both, up to n_seq) run as
+ * mr_paged_decode does where the lengths say that this reads little again; the choice depends on lengths, types and
+ * heads only.
+ * bf16 calls run on the tensor cores when page_rows is a multiple of 8, the rows of Q and O are 16-byte
+ * aligned (addresses and strides) and Q's strides are above 0.  Others, and fp32, run on the CUDA cores, which
+ * takes up to 30 times as long for many rows.
+ * Q holds total_q rows; those at or behind cu_q[n_seq] may be read and do not count.  O may be Q (the same tensor).
  */
 mr_status mr_paged_attn(const mr_kv_cache* cache, const mr_kv_seqs* seqs, const mr_rows* Q, int H_q,
                         const int32_t* cu_q, int total_q, float scale, int window, int sinks,
@@ -577,7 +584,8 @@ size_t mr_pages_copy_workspace_bytes(void);
  * All pairs count as copied at once, so a pair is skipped and MR_ERR_DEVICE_CHECK recorded when its
  * source or destination lies outside [0, n_pages), when its source is another pair's destination or when
  * an earlier pair has the same destination.  A pair of a page with itself does nothing and counts for nothing.
- * One source may go to many destinations.
+ * One source may go to many destinations.  Every block compares its pair with the whole list: up to a few
+ * thousand pairs this costs next to nothing, tens of thousands of small pages are quicker in several calls.
  */
 mr_status mr_pages_copy(void* const* pools, int n_pools, int64_t page_bytes, int64_t n_pages,
                         const int32_t* pairs, int n_pairs, void* ws, size_t ws_bytes, void* stream);
